@@ -22,7 +22,8 @@ import os
 __all__ = ["kda_get_workspace_size", "kda_chunk_prefill_fwd", "kda_status_string",
            "kda_workspace_status",
            "kda_last_hip_error", "kda_debug_set_vsplit", "kda_debug_set_kernel", "kda_debug_set_segment", "kda_debug_segment_length", "kda_debug_two_workgroups", "kda_spec_decode_step", "kda_chunk_prefill_fwd_noalloc", "kda_gate_proj",
-           "kda_gate_proj_workspace_size", "KdaError", "library_path", "load_library"]
+           "kda_gate_proj_workspace_size", "kda_gdr_get_workspace_size", "kda_gdr_prefill_fwd",
+           "kda_gdr_decode_step", "kda_add_rms_norm", "kda_w4_proj", "KdaError", "library_path", "load_library"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libkda.so")
@@ -39,6 +40,13 @@ class _Strides(ctypes.Structure):
     """kda_strides_t of include/kda.h (element strides)."""
     _fields_ = [(n, ctypes.c_int64) for n in (
         "q_token", "q_head", "k_token", "k_head", "v_token", "v_head", "g_token", "g_head",
+        "beta_token", "beta_head", "out_token", "out_head")]
+
+
+class _GdrStrides(ctypes.Structure):
+    """kda_gdr_strides_t of include/kda_layer.h (element strides)."""
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "q_token", "q_head", "k_token", "k_head", "v_token", "v_head", "a_token", "a_head",
         "beta_token", "beta_head", "out_token", "out_head")]
 
 
@@ -98,6 +106,19 @@ def load_library():
         lib.kda_spec_decode_step.argtypes = [P, P, P, P, P, P, P, F, F, P, I64, P, P, I32, P, P,
                                              P, P, I64, I32, I32, ctypes.c_int, SZ]
         lib.kda_spec_decode_step.restype = ctypes.c_int
+        lib.kda_gdr_get_workspace_size.argtypes = [I64, I32, I32, I32]
+        lib.kda_gdr_get_workspace_size.restype = SZ
+        lib.kda_gdr_prefill_fwd.argtypes = [P, P, P, P, P, P, P, F, P, P, P, P, P, P, I64, I32, I32,
+                                            I32, ctypes.c_int, SZ, ctypes.POINTER(_GdrStrides)]
+        lib.kda_gdr_prefill_fwd.restype = ctypes.c_int
+        lib.kda_gdr_decode_step.argtypes = [P, P, P, P, P, P, P, F, P, I64, P, P, P, I32, I32, I32,
+                                            ctypes.c_int, ctypes.POINTER(_GdrStrides)]
+        lib.kda_gdr_decode_step.restype = ctypes.c_int
+        lib.kda_add_rms_norm.argtypes = [P, P, P, F, P, P, P, I64, I32, I64, I64, I64, ctypes.c_int,
+                                         I32]
+        lib.kda_add_rms_norm.restype = ctypes.c_int
+        lib.kda_w4_proj.argtypes = [P, P, P, P, P, P, I32, I32, I32, I32, I64, I64]
+        lib.kda_w4_proj.restype = ctypes.c_int
         lib.kda_status_string.argtypes = [ctypes.c_int]
         lib.kda_status_string.restype = ctypes.c_char_p
         lib.kda_last_hip_error.argtypes = []
@@ -435,3 +456,211 @@ def kda_gate_proj(hidden, w_ab, w_b, p_ab, g, workspace, stream=None) -> None:
     if rc != KDA_OK:
         detail = lib.kda_last_hip_error().decode() if rc == 4 else ""
         raise KdaError(rc, f"kda_gate_proj: {kda_status_string(rc)} {detail}".strip())
+
+
+# ---- include/kda_layer.h: the operators around the forward --------------------
+
+def _on(t, name, dtype, shape, device, strided=False):
+    """Device pointer of t after its checks: dtype, shape, device, and dense
+    storage unless strided (then only the last of three dims must be dense)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not strided:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous (dense row-major)")
+    elif len(shape) == 3 and t.stride(2) != 1 and t.numel():
+        raise ValueError(f"{name} must have contiguous channels")
+    return t.data_ptr()
+
+
+def _gpu(t, name):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU device, got {t.device}")
+    return t.device
+
+
+def _call(name, fn, device, stream, before, after):
+    """fn(*before, stream, *after) on the tensors' device; raises on a refusal."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device).cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if device.index == torch.cuda.current_device():
+        rc = fn(*before, int(stream), *after)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*before, int(stream), *after)
+    if rc != KDA_OK:
+        detail = kda_last_hip_error() if rc == 4 else ""
+        raise KdaError(rc, f"{name}: {kda_status_string(rc)} {detail}".strip())
+
+
+def _state_dtype(t):
+    import torch
+    if t.dtype == torch.float32:
+        return KDA_STATE_FP32
+    if t.dtype == torch.bfloat16:
+        return KDA_STATE_BF16
+    raise TypeError(f"state dtype must be float32 or bfloat16, got {t.dtype}")
+
+
+def _gdr_rows(q, k, v, a, beta_logits, A_log, dt_bias, out):
+    """(pointers of the inputs, pointer of out, device, rows, key heads, value heads, strides or None)."""
+    import torch
+    dev = _gpu(q, "q")
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM:
+        raise ValueError(f"q must be [T, Hk, {HEAD_DIM}], got {tuple(q.shape)}")
+    if not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError(f"v must be [T, Hv, {HEAD_DIM}]")
+    T, hk, _ = q.shape
+    hv = v.shape[1]
+    bf = torch.bfloat16
+    rows, heads = (T, hk, HEAD_DIM), (T, hv, HEAD_DIM)
+    ptrs = [_on(q, "q", bf, rows, dev, True), _on(k, "k", bf, rows, dev, True),
+            _on(v, "v", bf, heads, dev, True), _on(a, "a", bf, (T, hv), dev, True),
+            _on(beta_logits, "beta_logits", bf, (T, hv), dev, True),
+            _on(A_log, "A_log", torch.float32, (hv,), dev),
+            _on(dt_bias, "dt_bias", torch.float32, (hv,), dev)]
+    o = _on(out, "out", bf, heads, dev, True)
+    st = None
+    views = (q, k, v, a, beta_logits, out)
+    if T and not all(t.is_contiguous() for t in views):
+        st = ctypes.byref(_GdrStrides(*(x for t in views for x in t.stride()[:2])))
+    return ptrs, o, dev, T, hk, hv, st
+
+
+def kda_gdr_get_workspace_size(max_tokens: int, key_heads: int, value_heads: int,
+                               max_seqs: int) -> int:
+    return int(load_library().kda_gdr_get_workspace_size(int(max_tokens), int(key_heads),
+                                                         int(value_heads), int(max_seqs)))
+
+
+def kda_gdr_prefill_fwd(q, k, v, a, beta_logits, A_log, dt_bias, scale: float, initial_state,
+                        cu_seqlens, out, final_state, workspace, stream=None) -> None:
+    """Queue one prefill of the gated delta rule with one decay per value head
+    (see include/kda_layer.h, kda_gdr_prefill_fwd).
+
+    q, k [T, Hk, 128], v, out [T, Hv, 128] bf16 and a, beta_logits [T, Hv] bf16,
+    strided views among them (channels contiguous, strides multiples of 8);
+    A_log, dt_bias [Hv] fp32; initial_state None or [N, Hv, 128, 128];
+    final_state [N, Hv, 128, 128] fp32 or bf16, initial_state's dtype (and may
+    be it); cu_seqlens [N + 1] int32; workspace uint8 of
+    kda_gdr_get_workspace_size(T, Hk, Hv, N) bytes, no initialisation needed;
+    stream as for kda_chunk_prefill_fwd.
+    """
+    import torch
+    lib = load_library()
+    ptrs, o, dev, T, hk, hv, st = _gdr_rows(q, k, v, a, beta_logits, A_log, dt_bias, out)
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be [N + 1] with N >= 1")
+    n = cu_seqlens.numel() - 1
+    shape = (n, hv, HEAD_DIM, HEAD_DIM)
+    sdt = _state_dtype(final_state)
+    s0 = None if initial_state is None else _on(initial_state, "initial_state", final_state.dtype,
+                                                shape, dev)
+    cu = _on(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), dev)
+    fs = _on(final_state, "final_state", final_state.dtype, shape, dev)
+    ws, size = None, 0
+    if workspace is not None:
+        ws, size = _on(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel()
+    _call("kda_gdr_prefill_fwd", lib.kda_gdr_prefill_fwd, dev, stream,
+          (*ptrs, float(scale), s0, cu, o, fs, ws), (T, hk, hv, n, sdt, size, st))
+
+
+def kda_gdr_decode_step(q, k, v, a, beta_logits, A_log, dt_bias, scale: float, state_pool,
+                        state_indices, out, stream=None) -> None:
+    """Queue one token of the gated delta rule for each of N sequences on a
+    pool of states, in place (see include/kda_layer.h, kda_gdr_decode_step).
+
+    q, k, v, a, beta_logits, out as for kda_gdr_prefill_fwd with T = N;
+    state_pool [num_slots, Hv, 128, 128] fp32 or bf16; state_indices [N] int32,
+    an index outside the pool marks a padding row.
+    """
+    import torch
+    lib = load_library()
+    ptrs, o, dev, n, hk, hv, st = _gdr_rows(q, k, v, a, beta_logits, A_log, dt_bias, out)
+    sdt = _state_dtype(state_pool)
+    if state_pool.dim() != 4:
+        raise ValueError("state_pool must be [num_slots, Hv, 128, 128]")
+    slots = state_pool.shape[0]
+    pool = _on(state_pool, "state_pool", state_pool.dtype, (slots, hv, HEAD_DIM, HEAD_DIM), dev)
+    idx = _on(state_indices, "state_indices", torch.int32, (n,), dev)
+    _call("kda_gdr_decode_step", lib.kda_gdr_decode_step, dev, stream,
+          (*ptrs, float(scale), pool, slots, idx, o), (n, hk, hv, sdt, st))
+
+
+def kda_add_rms_norm(x, residual, weight, eps: float, out, out_scale=None, group_size: int = 0,
+                     stream=None) -> None:
+    """Queue residual <- x + residual and out <- its RMS norm (see
+    include/kda_layer.h, kda_add_rms_norm).
+
+    x, residual (or None) [M, dim] bf16, rows may be strided; weight [dim]
+    bf16; out [M, dim] bf16, or float8_e4m3fn with out_scale fp32 [M, 1] (or
+    [M]; group_size 0) or [M, ceil(dim / 128)] (group_size 128).
+    """
+    import torch
+    lib = load_library()
+    dev = _gpu(x, "x")
+    if x.dim() != 2 or not isinstance(out, torch.Tensor):
+        raise ValueError("x and out must be [M, dim] tensors")
+    m, dim = x.shape
+    fp8 = out.dtype == torch.float8_e4m3fn
+    rows = []
+    for t, name, dtype in ((x, "x", torch.bfloat16), (residual, "residual", torch.bfloat16),
+                           (out, "out", torch.float8_e4m3fn if fp8 else torch.bfloat16)):
+        if t is None and name == "residual":
+            rows.append((None, 0))
+            continue
+        ptr = _on(t, name, dtype, (m, dim), dev, True)
+        if t.stride(1) != 1 and dim > 1 and m:
+            raise ValueError(f"{name} must have contiguous rows")
+        rows.append((ptr, t.stride(0)))
+    w = _on(weight, "weight", torch.bfloat16, (dim,), dev)
+    sc = None
+    if out_scale is not None:
+        groups = (dim + 127) // 128 if group_size else 1
+        shape = (m,) if out_scale.dim() == 1 and groups == 1 else (m, groups)
+        sc = _on(out_scale, "out_scale", torch.float32, shape, dev)
+    (xp, xs), (rp, rs), (op, os_) = rows
+    _call("kda_add_rms_norm", lib.kda_add_rms_norm, dev, stream, (xp, rp, w, float(eps), op, sc),
+          (m, dim, xs, rs, os_, 1 if fp8 else 0, int(group_size)))
+
+
+def kda_w4_proj(x, w, scales, zeros, y, group_size: int, stream=None) -> None:
+    """Queue y = x (4-bit weights)^T for at most 64 tokens (see
+    include/kda_layer.h, kda_w4_proj).
+
+    x [M, K] and y [M, N] bf16, rows may be strided; w [N, K / 2] uint8, even k
+    in the low four bits; scales [N, K / group_size] bf16; zeros the same or
+    None (8 everywhere).
+    """
+    import torch
+    lib = load_library()
+    dev = _gpu(x, "x")
+    if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("x and w must be 2-D tensors")
+    m, k = x.shape
+    n = w.shape[0]
+    if group_size not in (32, 64, 128) or k % group_size:
+        raise ValueError(f"group_size must be 32, 64 or 128 and divide {k}, got {group_size}")
+    bf = torch.bfloat16
+    xp, yp = _on(x, "x", bf, (m, k), dev, True), _on(y, "y", bf, (m, n), dev, True)
+    for t, name in ((x, "x"), (y, "y")):
+        if t.stride(1) != 1 and t.shape[1] > 1 and m:
+            raise ValueError(f"{name} must have contiguous rows")
+    wp = _on(w, "w", torch.uint8, (n, k // 2), dev)
+    sp = _on(scales, "scales", bf, (n, k // group_size), dev)
+    zp = None if zeros is None else _on(zeros, "zeros", bf, (n, k // group_size), dev)
+    _call("kda_w4_proj", lib.kda_w4_proj, dev, stream, (xp, wp, sp, zp, yp),
+          (m, k, n, int(group_size), x.stride(0), y.stride(0)))

@@ -18,6 +18,7 @@
 
 #include "kda.h"
 #include "kda_internal.h"
+#include "kda_layer_internal.h"
 
 namespace {
 
@@ -515,6 +516,11 @@ kda_status_t forward(const void* q, const void* k, const void* v, const void* g,
 }
 
 }  // namespace
+
+namespace kda {
+int record_hip_failure(hipError_t e, const char* step) { return hip_failure(e, step); }
+hipError_t device_cus(int* cus) { return device_cu_count(cus); }
+}  // namespace kda
 
 extern "C" {
 
