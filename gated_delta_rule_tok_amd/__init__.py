@@ -16,6 +16,7 @@ kda_chunk_prefill_fwd_strided, with no copy.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -459,84 +460,119 @@ def kda_gate_proj(hidden, w_ab, w_b, p_ab, g, workspace, stream=None) -> None:
 
 
 # ---- include/kda_layer.h: the operators around the forward --------------------
+#
+# Their calls take microseconds on the device, so the checks are kept short: a
+# tensor is compared as a whole in the path that passes, and what is wrong with
+# it is found out in _refuse.
 
-def _on(t, name, dtype, shape, device, strided=False):
-    """Device pointer of t after its checks: dtype, shape, device, and dense
-    storage unless strided (then only the last of three dims must be dense)."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if not strided:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous (dense row-major)")
-    elif len(shape) == 3 and t.stride(2) != 1 and t.numel():
-        raise ValueError(f"{name} must have contiguous channels")
-    return t.data_ptr()
+def _torch():
+    """torch, imported on first use (like load_library)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
-def _gpu(t, name):
-    import torch
+_torch_module = None
+
+
+def _refuse(t, name, dtype, shape, index):
+    """Raise what is wrong with t (see _on)."""
+    torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be on a GPU device, got {t.device}")
-    return t.device
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous (dense row-major)")
 
 
-def _call(name, fn, device, stream, before, after):
-    """fn(*before, stream, *after) on the tensors' device; raises on a refusal."""
-    import torch
+def _view(t, name, dtype, shape, index):
+    """Device pointer of t, whose strides are the caller's to look at."""
+    if not (isinstance(t, _torch_module.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == index):
+        _refuse(t, name, dtype, shape, index)
+    return t.data_ptr()
+
+
+def _on(t, name, dtype, shape, index):
+    """Device pointer of t: dense, of this dtype and shape, on GPU `index`."""
+    if not (isinstance(t, _torch_module.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == index and t.is_contiguous()):
+        _refuse(t, name, dtype, shape, index)
+    return t.data_ptr()
+
+
+def _gpu(t, name):
+    """Index of the GPU t is on."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU device, got {t.device}")
+    return t.get_device()
+
+
+def _call(name, fn, index, stream, before, after):
+    """fn(*before, stream, *after) on GPU `index`; raises on a refusal."""
+    cuda = _torch_module.cuda
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
-    elif isinstance(stream, torch.cuda.Stream):
+        stream = _torch_module._C._cuda_getCurrentRawStream(index)
+    elif isinstance(stream, cuda.Stream):
         stream = stream.cuda_stream
-    if device.index == torch.cuda.current_device():
-        rc = fn(*before, int(stream), *after)
+    if index == cuda.current_device():
+        rc = fn(*before, stream, *after)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*before, int(stream), *after)
+        with cuda.device(index):
+            rc = fn(*before, stream, *after)
     if rc != KDA_OK:
         detail = kda_last_hip_error() if rc == 4 else ""
         raise KdaError(rc, f"{name}: {kda_status_string(rc)} {detail}".strip())
 
 
 def _state_dtype(t):
-    import torch
-    if t.dtype == torch.float32:
+    torch = _torch()
+    dtype = t.dtype if isinstance(t, torch.Tensor) else type(t)
+    if dtype == torch.float32:
         return KDA_STATE_FP32
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return KDA_STATE_BF16
-    raise TypeError(f"state dtype must be float32 or bfloat16, got {t.dtype}")
+    raise TypeError(f"state dtype must be float32 or bfloat16, got {dtype}")
+
+
+@functools.lru_cache(maxsize=256)
+def _gdr_strides(*strides):
+    return _GdrStrides(*strides)
 
 
 def _gdr_rows(q, k, v, a, beta_logits, A_log, dt_bias, out):
-    """(pointers of the inputs, pointer of out, device, rows, key heads, value heads, strides or None)."""
-    import torch
+    """(pointers of the inputs, pointer of out, GPU, rows, key heads, value heads, strides or None)."""
     dev = _gpu(q, "q")
+    torch = _torch_module
+    bf, f32 = torch.bfloat16, torch.float32
     if q.dim() != 3 or q.shape[2] != HEAD_DIM:
         raise ValueError(f"q must be [T, Hk, {HEAD_DIM}], got {tuple(q.shape)}")
     if not isinstance(v, torch.Tensor) or v.dim() != 3:
         raise ValueError(f"v must be [T, Hv, {HEAD_DIM}]")
-    T, hk, _ = q.shape
+    T, hk, _ = rows = q.shape
     hv = v.shape[1]
-    bf = torch.bfloat16
-    rows, heads = (T, hk, HEAD_DIM), (T, hv, HEAD_DIM)
-    ptrs = [_on(q, "q", bf, rows, dev, True), _on(k, "k", bf, rows, dev, True),
-            _on(v, "v", bf, heads, dev, True), _on(a, "a", bf, (T, hv), dev, True),
-            _on(beta_logits, "beta_logits", bf, (T, hv), dev, True),
-            _on(A_log, "A_log", torch.float32, (hv,), dev),
-            _on(dt_bias, "dt_bias", torch.float32, (hv,), dev)]
-    o = _on(out, "out", bf, heads, dev, True)
+    heads, gates, per_head = (T, hv, HEAD_DIM), (T, hv), (hv,)
+    ptrs = (_view(q, "q", bf, rows, dev), _view(k, "k", bf, rows, dev), _view(v, "v", bf, heads, dev),
+            _view(a, "a", bf, gates, dev), _view(beta_logits, "beta_logits", bf, gates, dev),
+            _on(A_log, "A_log", f32, per_head, dev), _on(dt_bias, "dt_bias", f32, per_head, dev))
+    o = _view(out, "out", bf, heads, dev)
     st = None
-    views = (q, k, v, a, beta_logits, out)
-    if T and not all(t.is_contiguous() for t in views):
-        st = ctypes.byref(_GdrStrides(*(x for t in views for x in t.stride()[:2])))
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and a.is_contiguous()
+            and beta_logits.is_contiguous() and out.is_contiguous()):
+        sq, sk, sv, so = q.stride(), k.stride(), v.stride(), out.stride()
+        if not sq[2] == sk[2] == sv[2] == so[2] == 1:
+            raise ValueError("q, k, v and out must have contiguous channels")
+        st = _gdr_strides(*sq[:2], *sk[:2], *sv[:2], *a.stride(), *beta_logits.stride(), *so[:2])
     return ptrs, o, dev, T, hk, hv, st
 
 
@@ -559,9 +595,9 @@ def kda_gdr_prefill_fwd(q, k, v, a, beta_logits, A_log, dt_bias, scale: float, i
     kda_gdr_get_workspace_size(T, Hk, Hv, N) bytes, no initialisation needed;
     stream as for kda_chunk_prefill_fwd.
     """
-    import torch
     lib = load_library()
     ptrs, o, dev, T, hk, hv, st = _gdr_rows(q, k, v, a, beta_logits, A_log, dt_bias, out)
+    torch = _torch_module
     if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must be [N + 1] with N >= 1")
     n = cu_seqlens.numel() - 1
@@ -573,9 +609,10 @@ def kda_gdr_prefill_fwd(q, k, v, a, beta_logits, A_log, dt_bias, scale: float, i
     fs = _on(final_state, "final_state", final_state.dtype, shape, dev)
     ws, size = None, 0
     if workspace is not None:
-        ws, size = _on(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel()
+        size = workspace.numel()
+        ws = _on(workspace, "workspace", torch.uint8, (size,), dev)
     _call("kda_gdr_prefill_fwd", lib.kda_gdr_prefill_fwd, dev, stream,
-          (*ptrs, float(scale), s0, cu, o, fs, ws), (T, hk, hv, n, sdt, size, st))
+          (*ptrs, scale, s0, cu, o, fs, ws), (T, hk, hv, n, sdt, size, st))
 
 
 def kda_gdr_decode_step(q, k, v, a, beta_logits, A_log, dt_bias, scale: float, state_pool,
@@ -587,7 +624,6 @@ def kda_gdr_decode_step(q, k, v, a, beta_logits, A_log, dt_bias, scale: float, s
     state_pool [num_slots, Hv, 128, 128] fp32 or bf16; state_indices [N] int32,
     an index outside the pool marks a padding row.
     """
-    import torch
     lib = load_library()
     ptrs, o, dev, n, hk, hv, st = _gdr_rows(q, k, v, a, beta_logits, A_log, dt_bias, out)
     sdt = _state_dtype(state_pool)
@@ -595,9 +631,17 @@ def kda_gdr_decode_step(q, k, v, a, beta_logits, A_log, dt_bias, scale: float, s
         raise ValueError("state_pool must be [num_slots, Hv, 128, 128]")
     slots = state_pool.shape[0]
     pool = _on(state_pool, "state_pool", state_pool.dtype, (slots, hv, HEAD_DIM, HEAD_DIM), dev)
-    idx = _on(state_indices, "state_indices", torch.int32, (n,), dev)
+    idx = _on(state_indices, "state_indices", _torch_module.int32, (n,), dev)
     _call("kda_gdr_decode_step", lib.kda_gdr_decode_step, dev, stream,
-          (*ptrs, float(scale), pool, slots, idx, o), (n, hk, hv, sdt, st))
+          (*ptrs, scale, pool, slots, idx, o), (n, hk, hv, sdt, st))
+
+
+def _row_stride(t, name):
+    """Elements between the rows of a 2-D tensor whose rows are dense."""
+    row, col = t.stride()
+    if col != 1 and t.shape[1] > 1 and t.shape[0]:
+        raise ValueError(f"{name} must have contiguous rows")
+    return row
 
 
 def kda_add_rms_norm(x, residual, weight, eps: float, out, out_scale=None, group_size: int = 0,
@@ -609,32 +653,29 @@ def kda_add_rms_norm(x, residual, weight, eps: float, out, out_scale=None, group
     bf16; out [M, dim] bf16, or float8_e4m3fn with out_scale fp32 [M, 1] (or
     [M]; group_size 0) or [M, ceil(dim / 128)] (group_size 128).
     """
-    import torch
     lib = load_library()
     dev = _gpu(x, "x")
-    if x.dim() != 2 or not isinstance(out, torch.Tensor):
-        raise ValueError("x and out must be [M, dim] tensors")
-    m, dim = x.shape
-    fp8 = out.dtype == torch.float8_e4m3fn
-    rows = []
-    for t, name, dtype in ((x, "x", torch.bfloat16), (residual, "residual", torch.bfloat16),
-                           (out, "out", torch.float8_e4m3fn if fp8 else torch.bfloat16)):
-        if t is None and name == "residual":
-            rows.append((None, 0))
-            continue
-        ptr = _on(t, name, dtype, (m, dim), dev, True)
-        if t.stride(1) != 1 and dim > 1 and m:
-            raise ValueError(f"{name} must have contiguous rows")
-        rows.append((ptr, t.stride(0)))
-    w = _on(weight, "weight", torch.bfloat16, (dim,), dev)
+    torch = _torch_module
+    bf = torch.bfloat16
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M, dim], got {tuple(x.shape)}")
+    shape = x.shape
+    m, dim = shape
+    fp8 = isinstance(out, torch.Tensor) and out.dtype == torch.float8_e4m3fn
+    xp = _view(x, "x", bf, shape, dev)
+    op = _view(out, "out", torch.float8_e4m3fn if fp8 else bf, shape, dev)
+    rp = rs = 0
+    if residual is not None:
+        rp = _view(residual, "residual", bf, shape, dev)
+        rs = _row_stride(residual, "residual")
+    w = _on(weight, "weight", bf, (dim,), dev)
     sc = None
     if out_scale is not None:
         groups = (dim + 127) // 128 if group_size else 1
-        shape = (m,) if out_scale.dim() == 1 and groups == 1 else (m, groups)
-        sc = _on(out_scale, "out_scale", torch.float32, shape, dev)
-    (xp, xs), (rp, rs), (op, os_) = rows
-    _call("kda_add_rms_norm", lib.kda_add_rms_norm, dev, stream, (xp, rp, w, float(eps), op, sc),
-          (m, dim, xs, rs, os_, 1 if fp8 else 0, int(group_size)))
+        flat = groups == 1 and isinstance(out_scale, torch.Tensor) and out_scale.dim() == 1
+        sc = _on(out_scale, "out_scale", torch.float32, (m,) if flat else (m, groups), dev)
+    _call("kda_add_rms_norm", lib.kda_add_rms_norm, dev, stream, (xp, rp, w, eps, op, sc),
+          (m, dim, _row_stride(x, "x"), rs, _row_stride(out, "out"), 1 if fp8 else 0, group_size))
 
 
 def kda_w4_proj(x, w, scales, zeros, y, group_size: int, stream=None) -> None:
@@ -645,22 +686,20 @@ def kda_w4_proj(x, w, scales, zeros, y, group_size: int, stream=None) -> None:
     in the low four bits; scales [N, K / group_size] bf16; zeros the same or
     None (8 everywhere).
     """
-    import torch
     lib = load_library()
     dev = _gpu(x, "x")
+    torch = _torch_module
+    bf = torch.bfloat16
     if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("x and w must be 2-D tensors")
     m, k = x.shape
     n = w.shape[0]
     if group_size not in (32, 64, 128) or k % group_size:
         raise ValueError(f"group_size must be 32, 64 or 128 and divide {k}, got {group_size}")
-    bf = torch.bfloat16
-    xp, yp = _on(x, "x", bf, (m, k), dev, True), _on(y, "y", bf, (m, n), dev, True)
-    for t, name in ((x, "x"), (y, "y")):
-        if t.stride(1) != 1 and t.shape[1] > 1 and m:
-            raise ValueError(f"{name} must have contiguous rows")
-    wp = _on(w, "w", torch.uint8, (n, k // 2), dev)
-    sp = _on(scales, "scales", bf, (n, k // group_size), dev)
-    zp = None if zeros is None else _on(zeros, "zeros", bf, (n, k // group_size), dev)
-    _call("kda_w4_proj", lib.kda_w4_proj, dev, stream, (xp, wp, sp, zp, yp),
-          (m, k, n, int(group_size), x.stride(0), y.stride(0)))
+    per = (n, k // group_size)
+    ptrs = (_view(x, "x", bf, (m, k), dev), _on(w, "w", torch.uint8, (n, k // 2), dev),
+            _on(scales, "scales", bf, per, dev),
+            None if zeros is None else _on(zeros, "zeros", bf, per, dev),
+            _view(y, "y", bf, (m, n), dev))
+    _call("kda_w4_proj", lib.kda_w4_proj, dev, stream, ptrs,
+          (m, k, n, group_size, _row_stride(x, "x"), _row_stride(y, "y")))

@@ -221,8 +221,8 @@ kda_status_t kda_w4_proj(const void* x, const void* w, const void* scales, const
     return KDA_ERR_INVALID_ARG;
   if (num_tokens > 0 && (!x || !y)) return KDA_ERR_INVALID_ARG;
   if (misaligned(x, 16) || misaligned(y, 2)) return KDA_ERR_INVALID_ARG;
-  constexpr int64_t kMaxStride = int64_t(1) << 30;
-  if (num_tokens > 1 && (x_row < k || x_row % 8 || y_row < n || x_row > kMaxStride || y_row > kMaxStride))
+  // 32-bit byte offsets for the 64 rows of x
+  if (num_tokens > 1 && (x_row < k || x_row % 8 || x_row > (1 << 24) || y_row < n || y_row > (int64_t(1) << 30)))
     return KDA_ERR_INVALID_ARG;
   if (num_tokens == 0) return KDA_OK;
   kda::W4Params p{};

@@ -18,8 +18,12 @@
 // pairs (0,4), (1,5), (2,6), (3,7) out of a dword; x's operand is put into the
 // same order.
 //
-// The 8 waves of a workgroup take the 128-wide blocks of k in turn and add
-// their sums through LDS in wave order.
+// The waves of a workgroup share k, in runs of 128-wide blocks, and add their
+// sums through LDS in wave order.  What costs most beside the weights is x,
+// which every workgroup reads whole, and the scales; both go through LDS so
+// that their loads take whole cache lines.  16 tokens x 7168 x 14336 in groups
+// of 64 with zeros: 20.4 us (58 MB, 2.8 TB/s; a copy reaches 5.1); without the
+// loads of x and of the scales it took 14.
 #include "kda_layer_internal.h"
 #include "kda_mfma.h"
 
@@ -27,8 +31,6 @@ namespace kda {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-constexpr int kW4Waves = 8;
 
 // In: lane group g = l / 16 holds dwords j = 0..3 of its own piece; out: dword
 // j holds what dword g of group j held.
@@ -42,8 +44,8 @@ __device__ __forceinline__ u32x4 transpose4(u32x4 v) {
   return u32x4{c[0], c[1], d[0], d[1]};
 }
 
-__device__ __forceinline__ bf16x8 nibbles(uint32_t q) {
-  const uint32_t m = 0x000f000fu, e = 0x43004300u;
+__device__ __forceinline__ bf16x8 nibbles(uint32_t q, uint32_t e) {
+  const uint32_t m = 0x000f000fu;
   return __builtin_bit_cast(bf16x8, u32x4{(q & m) | e, ((q >> 4) & m) | e, ((q >> 8) & m) | e,
                                           ((q >> 12) & m) | e});
 }
@@ -55,96 +57,163 @@ __device__ __forceinline__ bf16x8 interleave(u32x4 x) {
                     __builtin_amdgcn_perm(x[3], x[1], 0x05040100), __builtin_amdgcn_perm(x[3], x[1], 0x07060302)});
 }
 
-// MT tiles of 16 tokens, NT tiles of 16 rows of w per workgroup; G the group.
-template <int MT, int NT, int G>
-__global__ __launch_bounds__(64 * kW4Waves) void w4_kernel(W4Params p) {
-  __shared__ f32x4 red[kW4Waves][MT * NT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// One 128-wide block of k as loaded: a lane's pieces of w and of x.
+template <int MT, int NT, int RQ>
+struct Block {
+  u32x4 w[NT], x[MT][RQ];
+};
+
+// MT tiles of 16 tokens (the first 4 RQ rows of each hold tokens), NT tiles of
+// 16 rows of w per workgroup, WAVES waves that share k, U blocks in flight per
+// wave; G the group.
+template <int MT, int RQ, int NT, int WAVES, int U, int G, bool ZERO>
+__global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Params p) {
+  constexpr int kGroups = 128 / G;  // groups in a block
+  constexpr int kSteps = G / 32;    // MFMA steps in a group
+  // groups whose scales and zeros are in LDS at a time
+  constexpr int kSegGroups = MT * NT > 4 ? 128 : 256, kScalePitch = kSegGroups + 1;
+  constexpr int kXBytes = WAVES * MT * 4096, kScaleBytes = 16 * NT * kScalePitch * 4;
+  constexpr int kRedBytes = WAVES * MT * NT * 64 * 16;
+  __shared__ __align__(16) char lds[kXBytes + kScaleBytes > kRedBytes ? kXBytes + kScaleBytes : kRedBytes];
+  uint32_t* sz = reinterpret_cast<uint32_t*>(lds + kXBytes);  // [16 NT][kScalePitch]: scale | zero << 16
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
   const int n0 = blockIdx.x * (16 * NT);
-  const int groups = p.K / G;
-  const uint8_t* wrow[NT];
-  const uint16_t *srow[NT], *zrow[NT];
+  const int groups = p.K / G, blocks = (p.K + 127) / 128;
+  // rows behind the last row or token repeat it: their sums are not stored
+  // (32-bit offsets from scalar bases: 64 rows of at most 2^19 bytes of w, and of 2^20 elements of x)
+  const uint8_t* wbase = p.w + size_t(n0) * (p.K / 2);
+  uint32_t wrow[NT], xrow[MT][RQ];
+  const int last = p.K % 128 ? p.K - p.K % 128 : p.K;  // where a block that is not whole begins
+  const uint32_t wpiece = 16 * g4, wtail = min(16 * g4, max(p.K - 32 - last, 0) / 2);
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int n = min(n0 + 16 * i + l16, p.N - 1);
-    wrow[i] = p.w + size_t(n) * (p.K / 2);
-    srow[i] = p.scales + size_t(n) * groups;
-    zrow[i] = p.zeros ? p.zeros + size_t(n) * groups : nullptr;
-  }
-  const uint16_t* xrow[MT];
-  bool mok[MT];
+  for (int i = 0; i < NT; ++i) wrow[i] = uint32_t(min(16 * i + l16, p.N - 1 - n0)) * uint32_t(p.K / 2);
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int m = 16 * i + l16;
-    mok[i] = m < p.M;
-    xrow[i] = p.x + size_t(mok[i] ? m : 0) * p.x_row;
-  }
-  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
-  constexpr int kGroups = 128 / G;   // groups in a block of 128
-  constexpr int kSteps = G / 32;     // MFMA steps in a group
-  f32x4 acc[MT][NT] = {};
-  for (int k0 = 128 * wave; k0 < p.K; k0 += 128 * kW4Waves) {
-    u32x4 w[NT];
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int k = k0 + 32 * g4;  // K % 32 == 0: a piece is inside or outside
-      w[i] = k < p.K ? *reinterpret_cast<const u32x4*>(wrow[i] + k / 2) : u32x4{};
-    }
-    float s[NT][kGroups], z[NT][kGroups];
+    for (int j = 0; j < RQ; ++j) xrow[i][j] = uint32_t(min(16 * i + 4 * j + g4, p.M - 1) * p.x_row);
+  const uint32_t xpiece = 8 * l16, xtail = min(8 * l16, max(p.K - 8 - last, 0));
+  // this wave's x, 256 bytes a row, its 16-byte pieces in the order piece ^ row (bank spread)
+  char* xl = lds + wave * (MT * 4096);
+  const uint32_t xread = l16 * 256;
+  typedef Block<MT, NT, RQ> B;
+  // Branch-free, so that the loads of U blocks stay in flight; in the last
+  // block of a K that is no multiple of 128 (it is one of 32) pieces behind it
+  // repeat the last one, and add() takes zeros for x there.
+  const auto load = [&](B& b, int blk) {
+    const int k0 = 128 * blk;
+    const uint32_t piece = k0 < last ? wpiece : wtail;
+    const uint8_t* wk = wbase + k0 / 2;
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < kGroups; ++j) {
-        const int g = min(k0 / G + j, groups - 1);
-        s[i][j] = bf16_to_f32(srow[i][g]);
-        z[i][j] = p.zeros ? bf16_to_f32(zrow[i][g]) : 8.f;
-      }
-    u32x4 x[MT][4];
+    for (int i = 0; i < NT; ++i) b.w[i] = *reinterpret_cast<const u32x4*>(wk + (wrow[i] + piece));
+    const uint16_t* xk = p.x + k0;
+    const uint32_t xp = k0 < last ? xpiece : xtail;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = k0 + 32 * j + 8 * g4;
-        x[i][j] = mok[i] && k < p.K ? *reinterpret_cast<const u32x4*>(xrow[i] + k) : u32x4{};
-      }
+      for (int j = 0; j < RQ; ++j) b.x[i][j] = *reinterpret_cast<const u32x4*>(xk + (xrow[i][j] + xp));
+  };
+  // 128 in both halves, in a vector register: an instruction reads one scalar
+  // only, so that two literals would make (q & m) | e two instructions
+  uint32_t e128 = 0x43004300u;
+  asm("" : "+v"(e128));
+  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+  f32x4 acc[MT][NT] = {};
+  const auto add = [&](B& b, int blk, int seg) {
+    // x through LDS into operands: a load of it takes whole lines of 4 rows, where loads
+    // in the operands' layout took half lines of 16 rows, at 2.5 times the cost
+    const bool in = 128 * blk + 8 * l16 < p.K;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) w[i] = transpose4(w[i]);
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < RQ; ++j) {
+        const int r = 4 * j + g4;
+        *reinterpret_cast<bf16x8*>(xl + i * 4096 + r * 256 + ((l16 ^ r) << 4)) =
+            interleave(in ? b.x[i][j] : u32x4{});
+      }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+    for (int i = 0; i < NT; ++i) b.w[i] = transpose4(b.w[i]);
 #pragma unroll
     for (int j = 0; j < kGroups; ++j) {
       f32x4 sx[MT] = {}, c[MT][NT] = {};
 #pragma unroll
       for (int q = 0; q < kSteps; ++q) {
         const int d = j * kSteps + q;
-        bf16x8 b[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) b[n] = nibbles(w[n][d]);
+        bf16x8 a[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          const bf16x8 a = interleave(x[m][d]);
-          sx[m] = mfma32(a, ones, sx[m]);
+          a[m] = *reinterpret_cast<const bf16x8*>(xl + m * 4096 + xread + (((4 * d + g4) ^ l16) << 4));
+          sx[m] = mfma32(a[m], ones, sx[m]);
+        }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) c[m][n] = mfma32(a, b[n], c[m][n]);
+        for (int n = 0; n < NT; ++n) {
+          const bf16x8 f = nibbles(b.w[n][d], e128);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) c[m][n] = mfma32(a[m], f, c[m][n]);
         }
       }
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t v = sz[(16 * n + l16) * kScalePitch + blk * kGroups + j - seg];
+        const float sc = bf16_lo(v), of = 128.f + bf16_hi(v);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            acc[m][n][r] += s[n][j] * (c[m][n][r] - (128.f + z[n][j]) * sx[m][r]);
+            acc[m][n][r] = fmaf(sc, fmaf(-of, sx[m][r], c[m][n][r]), acc[m][n][r]);
+      }
     }
+  };
+  // Segments of 256 groups, whose scales and zeros go through LDS (one per row
+  // and group straight into registers took longer than the weights: 16 lines
+  // per load of 2 bytes).  A wave's blocks of a segment are adjacent.  Every
+  // load is unconditional (the last block is repeated behind the end), so that
+  // the waits count loads, not branches.
+  for (int seg = 0; seg < groups; seg += kSegGroups) {
+    const int b0 = seg / kGroups, nb = min(blocks - b0, kSegGroups / kGroups);
+    const int per = (nb + WAVES - 1) / WAVES, first = b0 + wave * per;
+    const int cnt = max(0, min(per, b0 + nb - first));
+    B buf[U];
+    if (cnt) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) load(buf[u], first + min(u, cnt - 1));
+    }
+    if (seg) __syncthreads();
+    // groups behind the last one of its block of 128 count nothing
+    const int ns = min(groups - seg, kSegGroups), nz = (ns + kGroups - 1) / kGroups * kGroups;
+    for (int r = wave; r < 16 * NT; r += WAVES) {
+      const size_t row = size_t(min(n0 + r, p.N - 1)) * groups + seg;
+      for (int g = lane; g < nz; g += 64)
+        sz[r * kScalePitch + g] =
+            g < ns ? uint32_t(p.scales[row + g]) | (ZERO ? uint32_t(p.zeros[row + g]) << 16 : 0x41000000u) : 0u;
+    }
+    __syncthreads();
+    int i = 0;
+    for (; i + U < cnt; i += U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        add(buf[u], first + i + u, seg);
+        load(buf[u], first + min(i + u + U, cnt - 1));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u < cnt) add(buf[u], first + i + u, seg);
   }
+  __syncthreads();
+  f32x4(*red)[MT * NT][64] = reinterpret_cast<f32x4(*)[MT * NT][64]>(lds);
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) red[wave][m * NT + n][lane] = acc[m][n];
   __syncthreads();
-  for (int i = wave; i < MT * NT; i += kW4Waves) {
+  for (int i = wave; i < MT * NT; i += WAVES) {
     f32x4 y = red[0][i][lane];
 #pragma unroll
-    for (int u = 1; u < kW4Waves; ++u) y += red[u][i][lane];
+    for (int u = 1; u < WAVES; ++u) y += red[u][i][lane];
     const int n = n0 + 16 * (i % NT) + l16;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -154,22 +223,40 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_kernel(W4Params p) {
   }
 }
 
-template <int MT, int NT>
+template <int MT, int RQ, int NT, int WAVES, int U, int G>
+const void* kernel(bool zero) {
+  return zero ? reinterpret_cast<const void*>(&w4_kernel<MT, RQ, NT, WAVES, U, G, true>)
+              : reinterpret_cast<const void*>(&w4_kernel<MT, RQ, NT, WAVES, U, G, false>);
+}
+
+template <int MT, int RQ, int NT, int WAVES, int U>
 hipError_t launch(const W4Params& p, hipStream_t st) {
   W4Params arg = p;
   void* args[] = {&arg};
-  const void* f = p.group == 32   ? reinterpret_cast<const void*>(&w4_kernel<MT, NT, 32>)
-                  : p.group == 64 ? reinterpret_cast<const void*>(&w4_kernel<MT, NT, 64>)
-                                  : reinterpret_cast<const void*>(&w4_kernel<MT, NT, 128>);
-  return hipLaunchKernel(f, dim3((p.N + 16 * NT - 1) / (16 * NT)), dim3(64 * kW4Waves), args, 0, st);
+  const bool z = p.zeros != nullptr;
+  const void* f = p.group == 32   ? kernel<MT, RQ, NT, WAVES, U, 32>(z)
+                  : p.group == 64 ? kernel<MT, RQ, NT, WAVES, U, 64>(z)
+                                  : kernel<MT, RQ, NT, WAVES, U, 128>(z);
+  return hipLaunchKernel(f, dim3((p.N + 16 * NT - 1) / (16 * NT)), dim3(64 * WAVES), args, 0, st);
 }
 
 }  // namespace
 
+// Rows of w per workgroup: 32 read x half as often as 16, 16 give twice the
+// workgroups.  Measured (us, 16 / 32 rows): 16 tokens x 7168 x 1536 7.3 / 9.0,
+// x 2048 x 4096 4.8 / 5.5, x 4096 x 5120 8.6 / 8.0, x 7168 x 14336 26.9 / 20.4;
+// 64 x 7168 x 1536 20.0 / 23.8, 61 x 2048 x 7171 18.8 / 12.6; with at most 4
+// tokens x is a quarter of that: 4 x 7168 x 7168 11.3 / 11.5, 2 x 7168 x 14336
+// 17.2 / 15.8.  So 32 from half a workgroup of them per compute unit on, and
+// from one and a half on with at most 4 tokens.  64 rows lose everywhere.
 hipError_t launch_w4(const W4Params& p, int cus, hipStream_t stream) {
-  if (p.M <= 16) return launch<1, 1>(p, stream);
-  if (p.M <= 32) return launch<2, 2>(p, stream);
-  return launch<4, 2>(p, stream);
+  const int wide = (p.N + 31) / 32;
+  if (p.M <= 4)
+    return 2 * wide > 3 * cus ? launch<1, 1, 2, 8, 2>(p, stream) : launch<1, 1, 1, 8, 2>(p, stream);
+  const bool two = 2 * wide > cus;
+  if (p.M <= 16) return two ? launch<1, 4, 2, 8, 1>(p, stream) : launch<1, 4, 1, 16, 1>(p, stream);
+  if (p.M <= 32) return two ? launch<2, 4, 2, 8, 1>(p, stream) : launch<2, 4, 1, 8, 2>(p, stream);
+  return two ? launch<4, 4, 2, 8, 1>(p, stream) : launch<4, 4, 1, 8, 1>(p, stream);
 }
 
 }  // namespace kda

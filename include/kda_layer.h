@@ -169,7 +169,8 @@ kda_status_t kda_add_rms_norm(const void* x, void* residual, const void* weight,
  *
  *     y[m, n] = bf16( sum_k x[m, k] * (w[n, k] - z[n, g]) * scales[n, g] ),  g = k / group_size
  *
- *   x       bf16 [num_tokens, k], rows x_row elements apart (a multiple of 8)
+ *   x       bf16 [num_tokens, k], rows x_row elements apart (a multiple of
+ *           8, at most 2^24)
  *   w       uint8 [n, k / 2], dense: byte j of a row holds w[n, 2 j] in its
  *           low and w[n, 2 j + 1] in its high four bits, each 0..15
  *   scales  bf16 [n, k / group_size], dense
