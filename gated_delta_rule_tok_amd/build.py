@@ -34,6 +34,14 @@ HIPCC_FLAGS = [
     f"-I{CSRC}",
 ]
 
+# flags of single sources
+FILE_FLAGS = {
+    # MFMA results in the registers that the rest of the code can read: with the
+    # other half of the file free (one wave per SIMD) the compiler puts them there
+    # and moves every one of them back
+    "kda_gdr_chunk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+}
+
 
 def hipcc() -> str:
     path = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
@@ -48,7 +56,7 @@ def sources() -> list[str]:
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
-    cmd = [hipcc(), *HIPCC_FLAGS, "-c", src, "-o", obj]
+    cmd = [hipcc(), *HIPCC_FLAGS, *FILE_FLAGS.get(os.path.basename(src), []), "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{r.stdout}\n{r.stderr}")

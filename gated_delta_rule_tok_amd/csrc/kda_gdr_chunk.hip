@@ -11,34 +11,52 @@
 //
 // Two launches.  prep_kernel, one workgroup per (chunk, value head), forms
 // what does not depend on the state, for all chunks at once: T, the matrix P
-// in front of U, the coefficients of every token, and K transposed.
-// scan_kernel, one workgroup per (sequence, value head, slice of the value
-// columns), walks the chunks with the state in registers: four products per
-// chunk.
+// in front of U, the coefficients of every token, and K and Q as operands.
+// scan_kernel walks the chunks of a sequence with the state in registers.
 //
-// Precision.  q, k and v are bf16, so products with them take the raw rows
-// (exact operands) and fp32 norms and decays as coefficients on fp32 sums;
-// only S, R, U, T and P have to be rounded to become operands.  Each is cut
-// into NP bf16 pieces (x = x0 + x1 (+ x2), 8 bits each): NP = 3 for an fp32
-// state (24 bits, all of fp32), NP = 2 for a bf16 state (16 bits: 2^-17 per
-// factor, against the 2^-9 of the rounded state and output).  A product of two
-// cut factors sums the piece products i + j < NP.
+// Precision.  Operands are fp16 (11 bits), sums fp32.
+//  * A row of K or Q, times a power of two that brings its largest element to
+//    [1, 2), is exact in fp16 (bf16 has 8 bits; elements below 2^-14 of the
+//    largest are off by 2^-25 of it at most).  Norms, decays and the powers of
+//    two are fp32 coefficients on sums or on the other factor.
+//  * S, R, U and T have to be cut.  With an fp32 state each is two pieces,
+//    x = x0 + x1 (22 bits), and a product of two of them is x0 y0 + x0 y1 +
+//    x1 y0; with a bf16 state one piece: 2^-11 per factor beside the 2^-8 of
+//    the stored state.  out, which is bf16, takes one piece of S, U and P.
+//  * Range: everything in a column of the state (S, V, R, U) scales together,
+//    so each column carries a power of two per chunk that brings the larger of
+//    its |S| and |v| to [2^7, 2^8).  ||S_t|| grows by at most |v| per token
+//    (the map is a contraction), hence |U| <= (1 + sqrt(128) + 64) 2^8 < 2^15:
+//    no finite input overflows, and what fp16 loses below 2^-14 is under 2^-32
+//    of the column's largest element.  T and P are at most 1.
+#include <type_traits>
+
 #include "kda_gdr.h"
 
 namespace kda {
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
 constexpr int kC = kGdrChunk;
 constexpr int kUnits = 6;        // 16 x 32 pieces of a lower triangle of 64: row tile w has w / 2 + 1
-constexpr int kUnit = 64 * 8;    // bf16 of one such operand unit (1 KB)
-constexpr int kMaxPieces = 3;
-constexpr int kTriElems = 2 * kUnits * kMaxPieces * kUnit;  // T and P of one (chunk, head)
-constexpr int kCoefs = 5 * kC;   // floats of one (chunk, head)
-// coefficient rows: beta; beta e^G rk; scale e^G rq; rk e^(G_C - G); e^(G_C)
+constexpr int kKUnits = 16, kHeadUnits = 3 * kKUnits;  // K, Q and K^T of one (chunk, key head)
+constexpr int kMaxTri = 3 * kUnits;  // T in two pieces and P, of one (chunk, value head)
+constexpr int kCoefs = 5 * kC;   // floats of one (chunk, value head)
+// coefficient rows, rk and rq the factors that make a scaled row a unit one:
+// beta; beta e^G rk; e^G rq; rk e^(G_C - G); e^(G_C)
 enum { kBeta, kKs, kQs, kUs, kEnd };
 
+__device__ __forceinline__ f32x4 mfma32h(f16x8 a, f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
 __device__ __forceinline__ f32x4 mfma4(float a, float b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f16x8 cath(f16x4 lo, f16x4 hi) {
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 // First slot of sequence n (see GdrLayout).
@@ -46,31 +64,46 @@ __device__ __forceinline__ int64_t first_slot(const GdrParams& p, int n) {
   return int64_t(min(max(p.cu[n], 0), p.T)) / kC + n;
 }
 
-// x as NP bf16 pieces
+// NP fp16 pieces of four numbers
 template <int NP>
-__device__ __forceinline__ void cut(float x, bf16* o) {
+__device__ __forceinline__ void cut4(f32x4 x, f16x4* o) {
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    o[i] = (bf16)x;
-    x -= (float)o[i];
+    const f16x2 a = __builtin_convertvector((f32x2{x[0], x[1]}), f16x2);
+    const f16x2 b = __builtin_convertvector((f32x2{x[2], x[3]}), f16x2);
+    o[i] = f16x4{a[0], a[1], b[0], b[1]};
+    if (i + 1 < NP) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = fmaf(float(o[i][j]), -1.f, x[j]);
+    }
   }
 }
 
-// unit index of (row tile w, k-step s)
-__device__ __forceinline__ int unit_of(int w, int s) { return (w < 2 ? w : 2 * w - 2) + s; }
+// unit index of (row tile w, k-step s) in a triangle
+__device__ __forceinline__ constexpr int unit_of(int w, int s) { return (w < 2 ? w : 2 * w - 2) + s; }
 
 // ---- prep -------------------------------------------------------------------
 
 constexpr int kPitch = 68;  // floats per row of the LDS matrices (bank spread)
 
 struct PrepLds {
-  uint4 kf[4][4][64];       // K as operand units [tile][k-step][lane]
+  union {
+    bf16x8 kf[4][4][64];    // K as operand units [tile][k-step][lane], until A and P are formed
+    struct {
+      _Float16 P[kC][72];
+      float tmp[4][16][17];
+    };
+  };
   float A[kC][kPitch];      // A below the diagonal; T in the diagonal blocks; T_ij in block (j, i)
-  float P[kC][kPitch];
-  float tmp[4][16][17];
   double G[kC];
-  float rk[kC], rq[kC], beta[kC];
+  float rk[kC], rq[kC], beta[kC], kd[kC], qd[kC];
 };
+
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // acc += X Y for 16 x 16 fp32 blocks in LDS
 __device__ __forceinline__ f32x4 block_mul(const float* X, int xp, const float* Y, int yp, f32x4 acc,
@@ -80,74 +113,100 @@ __device__ __forceinline__ f32x4 block_mul(const float* X, int xp, const float* 
   return acc;
 }
 
-template <int NP>
-__device__ __forceinline__ void store_unit(uint16_t* base, int unit, int lane, const float* f) {
-  bf16 o[8][NP];
+// One row of K or Q: this lane's 32 channels (32 s + 8 g4 ..), the factor that
+// makes it a unit row, and the power of two that brings its largest element to
+// [1, 2).
+__device__ __forceinline__ void load_row(const uint16_t* row, bool ok, bf16x8 (&out)[4], float& unit, float& down) {
+  float sum = 0.f, big = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) cut<NP>(f[j], o[j]);
+  for (int s = 0; s < 4; ++s) {
+    const uint4 raw = *reinterpret_cast<const uint4*>(row + 32 * s);
+    float f[8];
+    unpack8(raw, f);
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const bf16x8 v = {o[0][i], o[1][i], o[2][i], o[3][i], o[4][i], o[5][i], o[6][i], o[7][i]};
-    *reinterpret_cast<bf16x8*>(base + (size_t(unit) * NP + i) * kUnit + lane * 8) = v;
+    for (int j = 0; j < 8; ++j) {
+      sum = fmaf(f[j], f[j], sum);
+      big = fmaxf(big, fabsf(f[j]));
+    }
+    out[s] = __builtin_bit_cast(bf16x8, raw);
   }
+  sum += __shfl_xor(sum, 16);
+  big = fmaxf(big, __shfl_xor(big, 16));
+  sum += __shfl_xor(sum, 32);
+  big = fmaxf(big, __shfl_xor(big, 32));
+  const uint32_t e = __float_as_uint(big) >> 23;  // 0: nothing but zeros (or less than fp32 squares hold)
+  down = e ? __uint_as_float((254u - min(e, 253u)) << 23) : 1.f;
+  unit = ok ? 1.f / sqrtf(sum + kNormEps) : 0.f;
+}
+
+// Eight bf16 times a power of two, in fp16
+__device__ __forceinline__ f16x8 scaled_half(bf16x8 raw, float down) {
+  const u32x4 x = __builtin_bit_cast(u32x4, raw);
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{bf16_lo(x[i]) * down, bf16_hi(x[i]) * down}), f16x2));
+  return __builtin_bit_cast(f16x8, o);
 }
 
 template <int NP>
-__global__ __launch_bounds__(256) void prep_kernel(GdrParams p, GdrLayout lay) {
+__global__ __launch_bounds__(256, 4) void prep_kernel(GdrParams p, GdrLayout lay) {
   __shared__ PrepLds L;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, l16 = lane & 15, g4 = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t slot = blockIdx.x / p.Hv;
-  const int h = blockIdx.x % p.Hv, group = p.Hv / p.Hk, hk = h / group;
-  int lo = 0, hi = p.N - 1;  // the last sequence whose first slot is not behind this one
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (first_slot(p, mid) <= slot) lo = mid; else hi = mid - 1;
+  const int h = blockIdx.x % p.Hv, hk = h / (p.Hv / p.Hk);
+  // the last sequence whose first slot is not behind this one, 64 candidates at a time
+  int lo = 0;
+  for (int span = p.N; span > 1;) {
+    const int step = (span + 63) / 64, n = lo + lane * step;
+    const bool in = lane * step < span && first_slot(p, min(n, p.N - 1)) <= slot;
+    const int k = 63 - __builtin_clzll(__ballot(in) | 1);
+    lo += k * step;
+    span = min(step, span - k * step);
   }
+  lo = __builtin_amdgcn_readfirstlane(lo);
   int t0, t1;
   gdr_range(p, lo, t0, t1);
   const int64_t off = (slot - first_slot(p, lo)) * kC;
   if (off < 0 || off >= t1 - t0) return;  // no chunk has this slot
   t0 += int(off);
   const int len = min(kC, t1 - t0);
+  const bool first = h % (p.Hv / p.Hk) == 0;  // writes K, Q and K^T for the key head's value heads
+  f16x8* units = reinterpret_cast<f16x8*>(p.ws + lay.head) + (size_t(slot) * p.Hk + hk) * (kHeadUnits * 64) + lane;
 
-  // rows of K and Q as operands: lane l row l % 16 of tile w, channels 32 s + 8 (l / 16)
+  // rows of K and Q as operands: lane l row l % 16 of tile w, channels 32 s + 8
+  // (l / 16); rows behind the end repeat the last one, with factors of 0
   bf16x8 kf[4], qf[4];
   {
     const int r = 16 * w + l16;
-    const bool ok = r < len;
-    const int64_t t = t0 + (ok ? r : 0);
-    const uint16_t* kp = p.k + t * p.k_t + hk * p.k_h + 8 * g4;
-    const uint16_t* qp = p.q + t * p.q_t + hk * p.q_h + 8 * g4;
-    float sk = 0.f, sq = 0.f;
+    const int64_t t = t0 + min(r, len - 1);
+    float rk, rq, kd, qd;
+    load_row(p.k + t * p.k_t + hk * p.k_h + 8 * g4, r < len, kf, rk, kd);
+    load_row(p.q + t * p.q_t + hk * p.q_h + 8 * g4, r < len, qf, rq, qd);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const uint4 a = ok ? *reinterpret_cast<const uint4*>(kp + 32 * s) : uint4{0, 0, 0, 0};
-      const uint4 b = ok ? *reinterpret_cast<const uint4*>(qp + 32 * s) : uint4{0, 0, 0, 0};
-      L.kf[w][s][lane] = a;
-      kf[s] = __builtin_bit_cast(bf16x8, a);
-      qf[s] = __builtin_bit_cast(bf16x8, b);
-      float f[8];
-      unpack8(a, f);
+    for (int s = 0; s < 4; ++s) L.kf[w][s][lane] = kf[s];
+    if (first) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sk = fmaf(f[j], f[j], sk);
-      unpack8(b, f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sq = fmaf(f[j], f[j], sq);
+      for (int s = 0; s < 4; ++s) {
+        units[(4 * w + s) * 64] = scaled_half(kf[s], kd);
+        units[(kKUnits + 4 * w + s) * 64] = scaled_half(qf[s], qd);
+      }
     }
-    sk += __shfl_xor(sk, 16);
-    sq += __shfl_xor(sq, 16);
-    sk += __shfl_xor(sk, 32);
-    sq += __shfl_xor(sq, 32);
     if (g4 == 0) {
-      L.rk[r] = ok ? 1.f / sqrtf(sk + kNormEps) : 0.f;
-      L.rq[r] = ok ? 1.f / sqrtf(sq + kNormEps) : 0.f;
+      L.rk[r] = rk;
+      L.rq[r] = rq;
+      L.kd[r] = kd;
+      L.qd[r] = qd;
     }
   }
-  if (w == 0) {  // gates: lane = token; G in fp64, so that differences of large sums keep their small terms
+  // gates: lane = token; G in fp64, so that differences of large sums keep their
+  // small terms, and times log2(e)
+  if (w == 0) {
     const bool ok = lane < len;
     const int64_t t = t0 + (ok ? lane : 0);
     const float la = gdr_log_decay(bf16_to_f32(p.a[t * p.a_t + h * p.a_h]), p.A_log[h], p.dt_bias[h]);
-    double G = ok ? double(la) : 0.0;
+    double G = ok ? double(la) * 1.4426950408889634074 : 0.0;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const double u = __shfl_up(G, o);
@@ -157,60 +216,75 @@ __global__ __launch_bounds__(256) void prep_kernel(GdrParams p, GdrLayout lay) {
     L.beta[lane] = ok ? gdr_sigmoid(bf16_to_f32(p.beta[t * p.b_t + h * p.b_h])) : 0.f;
   }
   __syncthreads();
-  // K transposed, as operand units [tile of 16 channels][k-step of 32 tokens]: lane l channel l % 16,
-  // tokens 32 s + 8 (l / 16); once per key head
-  if (h % group == 0) {
-    uint16_t* kt = reinterpret_cast<uint16_t*>(p.ws + lay.kt) + (size_t(slot) * p.Hk + hk) * (kD * kC);
+  // K transposed, as operand units [state tile r][k-step z]: lane l the channel
+  // of row l % 16 of tile r (see scan_kernel), tokens 32 z + 4 (l / 16) .. + 3
+  // and 16 further on
+  if (first) {
     const uint16_t* kl = reinterpret_cast<const uint16_t*>(&L.kf[0][0][0]);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int unit = 4 * w + u, c = 16 * (unit >> 1) + l16, tok = 32 * (unit & 1) + 8 * g4;
-      uint16_t e[8];
+      const int unit = 4 * w + u, r = unit >> 1;
+      const int c = 32 * (r >> 1) + 8 * (l16 >> 2) + 4 * (r & 1) + (l16 & 3);
+      f16x8 e;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)  // token t's channel c: tile t / 16, k-step c / 32, lane t % 16 + 16 (c / 8 % 4)
-        e[j] = kl[((((tok + j) >> 4) * 4 + (c >> 5)) * 64 + ((tok + j) & 15) + 16 * ((c >> 3) & 3)) * 8 + (c & 7)];
-      *reinterpret_cast<uint4*>(kt + unit * kUnit + lane * 8) =
-          uint4{uint32_t(e[0]) | uint32_t(e[1]) << 16, uint32_t(e[2]) | uint32_t(e[3]) << 16,
-                uint32_t(e[4]) | uint32_t(e[5]) << 16, uint32_t(e[6]) | uint32_t(e[7]) << 16};
+      for (int j = 0; j < 8; ++j) {
+        // token t's channel c: tile t / 16, k-step c / 32, lane t % 16 + 16 (c / 8 % 4)
+        const int tile = 2 * (unit & 1) + (j >> 2), row = 4 * g4 + (j & 3);
+        const uint16_t k = kl[((tile * 4 + (c >> 5)) * 64 + row + 16 * ((c >> 3) & 3)) * 8 + (c & 7)];
+        e[j] = (_Float16)(bf16_to_f32(k) * L.kd[16 * tile + row]);
+      }
+      units[(2 * kKUnits + unit) * 64] = e;
     }
   }
   const double Gend = L.G[kC - 1];  // tokens behind the end add nothing
   if (tid < kC) {
-    const float eG = expf(float(L.G[tid])), rk = L.rk[tid], b = L.beta[tid];
+    const float eG = ex2(float(L.G[tid])), b = L.beta[tid], kd = L.kd[tid], qd = L.qd[tid];
+    const float rk = L.rk[tid] / kd, rq = L.rq[tid] / qd;  // powers of two: exact
     float* co = reinterpret_cast<float*>(p.ws + lay.coef) + (size_t(slot) * p.Hv + h) * kCoefs + tid;
     co[kBeta * kC] = b;
     co[kKs * kC] = b * eG * rk;
-    co[kQs * kC] = p.scale * eG * L.rq[tid];
-    co[kUs * kC] = rk * expf(float(Gend - L.G[tid]));
-    co[kEnd * kC] = expf(float(Gend));
+    co[kQs * kC] = eG * rq;
+    co[kUs * kC] = rk * ex2(float(Gend - L.G[tid]));
+    co[kEnd * kC] = ex2(float(Gend));
   }
   // A and P, row tile w
+  f32x4 kk[4], qk[4];
+#pragma unroll
   for (int j = 0; j < 4; ++j) {
-    f32x4 kk = {}, qk = {};
+    kk[j] = qk[j] = f32x4{};
     if (j <= w) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const bf16x8 b = __builtin_bit_cast(bf16x8, L.kf[j][s][lane]);
-        kk = mfma32(kf[s], b, kk);
-        qk = mfma32(qf[s], b, qk);
+        const bf16x8 b = L.kf[j][s][lane];
+        kk[j] = mfma32(kf[s], b, kk[j]);
+        qk[j] = mfma32(qf[s], b, qk[j]);
       }
     }
+  }
+  __syncthreads();  // kf is read: P takes its place
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
     const int s = 16 * j + l16;
+    if (j > w) {  // P's unit of 32 columns may reach one tile further than the triangle
+      if (j == w + 1 && j % 2 == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) L.P[16 * w + 4 * g4 + i][s] = 0;
+      }
+      continue;
+    }
     const double Gs = L.G[s];
     const float rs = L.rk[s];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = 16 * w + 4 * g4 + i;
-      const float e = s <= t ? expf(float(L.G[t] - Gs)) * rs : 0.f;
-      if (j <= w) L.A[t][s] = s < t ? L.beta[t] * L.rk[t] * e * kk[i] : 0.f;
-      L.P[t][s] = s <= t ? p.scale * L.rq[t] * e * qk[i] : 0.f;
+      const float e = ex2(float(L.G[t] - Gs)) * rs;
+      L.A[t][s] = s < t ? L.beta[t] * L.rk[t] * e * kk[j][i] : 0.f;
+      L.P[t][s] = (_Float16)(s <= t ? L.rq[t] * e * qk[j][i] : 0.f);
     }
   }
   // T: the diagonal blocks by forward substitution, a column per lane
   {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    wave_sync();
     float x[16];
     const float* a = &L.A[16 * w][16 * w];
 #pragma unroll
@@ -220,8 +294,7 @@ __global__ __launch_bounds__(256) void prep_kernel(GdrParams p, GdrLayout lay) {
       for (int j = 0; j < i; ++j) v = fmaf(-a[i * kPitch + j], x[j], v);
       x[i] = v;
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     if (g4 == 0) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) L.A[16 * w + i][16 * w + l16] = x[i];
@@ -239,217 +312,305 @@ __global__ __launch_bounds__(256) void prep_kernel(GdrParams p, GdrLayout lay) {
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) L.tmp[w][4 * g4 + i][l16] = acc[i];
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      wave_sync();
       const f32x4 t = block_mul(&L.A[16 * w][16 * w], kPitch, &L.tmp[w][0][0], 17, f32x4{}, l16, g4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) L.A[16 * j + 4 * g4 + i][16 * w + l16] = -t[i];
     }
   }
   __syncthreads();
-  // T and P as operand units of row tile w
-  uint16_t* tri = reinterpret_cast<uint16_t*>(p.ws + lay.tri) + (size_t(slot) * p.Hv + h) * kTriElems;
+  // T and P as operand units of row tile w: slots 4 half .. are tokens 16 (2 s + half) + 4 g4 ..
+  f16x8* tri = reinterpret_cast<f16x8*>(p.ws + lay.tri) + (size_t(slot) * p.Hv + h) * (kMaxTri * 64) + lane;
   for (int s = 0; s <= w / 2; ++s) {
-    const int c0 = 32 * s + 8 * g4, cb = c0 >> 4;
-    float f[8];
-    const float* src = cb < w ? &L.A[16 * cb + l16][16 * w + (c0 & 15)] : &L.A[16 * w + l16][c0];
+    f16x4 t[2][NP], pp[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = cb <= w ? src[j] : 0.f;
-    store_unit<NP>(tri, unit_of(w, s), lane, f);
+    for (int half = 0; half < 2; ++half) {
+      const int cb = 2 * s + half;
+      const float* src = cb < w ? &L.A[16 * cb + l16][16 * w + 4 * g4] : &L.A[16 * w + l16][16 * cb + 4 * g4];
+      const f32x4 f = cb <= w ? f32x4{src[0], src[1], src[2], src[3]} : f32x4{};
+      cut4<NP>(f, t[half]);
+      pp[half] = *reinterpret_cast<const f16x4*>(&L.P[16 * w + l16][16 * cb + 4 * g4]);
+    }
+    const int u = unit_of(w, s);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = L.P[16 * w + l16][c0 + j];
-    store_unit<NP>(tri + kUnits * kMaxPieces * kUnit, unit_of(w, s), lane, f);
+    for (int i = 0; i < NP; ++i) tri[(u * NP + i) * 64] = cath(t[0][i], t[1][i]);
+    tri[(kUnits * NP + u) * 64] = cath(pp[0], pp[1]);
   }
 }
 
 // ---- scan -------------------------------------------------------------------
+//
+// A wave owns 16 value columns of one state for the whole sequence and
+// needs nothing of the other waves' columns: S, R and U stay in its registers
+// from the accumulators of one product to the operands of the next, without
+// LDS.  An accumulator tile holds, in lane l, rows 4 (l / 16) + i of column l %
+// 16; an operand takes 8 k-slots per lane, in any order that both operands
+// share.  Two accumulator tiles side by side are such an operand, with the k
+// order "4 (l / 16) + i of the first tile, then of the second": T, P and K^T
+// are laid out that way by prep_kernel.  For K and Q, whose units hold 8
+// adjacent channels per lane, the state's rows are permuted instead: row 4 g +
+// i of state tile r is channel 32 (r / 2) + 8 g + 4 (r % 2) + i.
+//
+// K, Q, K^T, T and P are operands of every wave alike: the workgroup stages a
+// chunk's units (1 KB each, in lane order) in LDS, the next chunk's while this
+// one is computed, by loads that write LDS directly; one barrier per chunk.
 
-constexpr int kSPitch = kD + 8;  // bf16 per column of the state's pieces
-constexpr int kUPitch = kC + 8;  // bf16 per column of the chunk's R and U
+// s_waitcnt operands: at most 0 or 16 vector memory accesses outstanding, the
+// other counters as they are (vmcnt in bits 3:0 and 15:14)
+constexpr int kVmcnt0 = 0x0f70, kVmcnt16 = 0x4f70;
 
-template <int NP, int CT>
-struct ScanLds {
-  bf16 S[NP][16 * CT][kSPitch];
-  bf16 R[NP][16 * CT][kUPitch];
-  bf16 U[NP][16 * CT][kUPitch];
-  bf16 W[NP][16 * CT][kUPitch];  // U with the coefficients of the state's update
+template <int NP>
+struct Stage {
+  static constexpr int kTri = kUnits * (NP + 1), kAll = kHeadUnits + kTri;
+  u32x4 unit[kAll][64];
+  f32x4 coef[kCoefs / 4 + 48];  // two loads of 64 lanes
 };
 
-template <int NP, int PITCH, int COLS>
-__device__ __forceinline__ void put4(bf16 (&dst)[NP][COLS][PITCH], int col, int row, f32x4 x) {
-  bf16 o[4][NP];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) cut<NP>(x[i], o[i]);
-#pragma unroll
-  for (int i = 0; i < NP; ++i) *reinterpret_cast<bf16x4*>(&dst[i][col][row]) = bf16x4{o[0][i], o[1][i], o[2][i], o[3][i]};
+constexpr int kRsrcWord3 = 0x00020000;  // raw buffer, 32-bit offsets
+// 16 bytes per lane from base + off + 16 * lane (off scalar) to dst + 16 * lane
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const char* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, -1, kRsrcWord3);
+}
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t base, int off, void* dst, int lane16) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(base, (__attribute__((address_space(3))) void*)dst, 16, lane16, off, 0, 0);
 }
 
-// acc[ct] += X Y, X in NP-piece operand units, Y in columns of LDS
-template <int NP, int CT>
-__device__ __forceinline__ void tri_mul(f32x4 (&acc)[CT], const bf16x8 (&x)[2][NP],
-                                        const bf16 (&y)[NP][16 * CT][kUPitch], int steps, int l16, int g4) {
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    if (s < steps) {
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int b = 0; b < NP; ++b) {
-          const bf16x8 f = *reinterpret_cast<const bf16x8*>(&y[b][16 * ct + l16][32 * s + 8 * g4]);
-#pragma unroll
-          for (int a = 0; a + b < NP; ++a) acc[ct] = mfma32(x[s][a], f, acc[ct]);
-        }
-    }
-  }
+// The largest of a lane's |x| and of the lanes that share its column
+__device__ __forceinline__ float over_column(float m) {
+  m = fmaxf(m, __shfl_xor(m, 16));
+  return fmaxf(m, __shfl_xor(m, 32));
 }
 
-// One token row operand of K or Q
-__device__ __forceinline__ void load_rows(bf16x8 (&f)[4], const uint16_t* base, bool ok) {
-#pragma unroll
-  for (int s = 0; s < 4; ++s)
-    f[s] = ok ? *reinterpret_cast<const bf16x8*>(base + 32 * s) : bf16x8{};
-}
-
-template <int NP, int CT>
-__global__ __launch_bounds__(256) void scan_kernel(GdrParams p, GdrLayout lay) {
-  __shared__ __align__(16) ScanLds<NP, CT> L;
-  constexpr int kSlices = kD / (16 * CT);
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, l16 = lane & 15, g4 = lane >> 4;
-  const int item = work_item(blockIdx.x, gridDim.x, kSlices);
-  const int n = item / (kSlices * p.Hv), h = item / kSlices % p.Hv, hk = h / (p.Hv / p.Hk);
-  const int col0 = item % kSlices * (16 * CT);
+template <int NP, int W>
+__global__ __launch_bounds__(64 * W, W / 4) void scan_kernel(GdrParams p, GdrLayout lay) {
+  __shared__ Stage<NP> L[2];
+  constexpr int kSlices = kD / (16 * W);
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = p.Hv / p.Hk;
+  // the value heads of a key head on one XCD: its units of K and Q are in that L2
+  const int item = work_item(blockIdx.x, gridDim.x, kSlices * group);
+  const int n = item / (kSlices * p.Hv), h = item / kSlices % p.Hv, hk = h / group;
+  const int col = (item % kSlices * W + w) * 16 + l16;  // this lane's value column
   int t0, t1;
   gdr_range(p, n, t0, t1);
   const int nc = (t1 - t0 + kC - 1) / kC;
 
-  // the state: key channels 32 w + 16 r + 4 g4 + i, columns col0 + 16 ct + l16
-  f32x4 S[2][CT];
-  const size_t sbase = (size_t(n) * p.Hv + h) * (kD * kD) + col0 + l16;
+  f32x4 S[8];                // the column's state times sc
+  float sc = 1.f, inv = 1.f;  // a power of two and its inverse
+  const size_t sbase = (size_t(n) * p.Hv + h) * (kD * kD) + col;
+  const auto state_at = [&](int r, int i) {
+    return sbase + size_t(32 * (r >> 1) + 8 * g4 + 4 * (r & 1) + i) * kD;
+  };
+  if (!p.s0) {
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < 8; ++r) S[r] = f32x4{};
+  } else if (p.state_bf16) {
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
+    for (int r = 0; r < 8; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const size_t e = sbase + size_t(32 * w + 16 * r + 4 * g4 + i) * kD + 16 * ct;
-        S[r][ct][i] = !p.s0 ? 0.f
-                            : p.state_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p.s0)[e])
-                                           : static_cast<const float*>(p.s0)[e];
-      }
-  const int64_t slot0 = first_slot(p, n);
-  const uint16_t* ktb = reinterpret_cast<const uint16_t*>(p.ws + lay.kt) + (size_t(slot0) * p.Hk + hk) * (kD * kC) + lane * 8;
-  const uint16_t* trib = reinterpret_cast<const uint16_t*>(p.ws + lay.tri) + (size_t(slot0) * p.Hv + h) * kTriElems + lane * 8;
-  const float* cob = reinterpret_cast<const float*>(p.ws + lay.coef) + (size_t(slot0) * p.Hv + h) * kCoefs;
-  const int steps = w / 2 + 1;
-
-  for (int c = 0; c < nc; ++c) {
-    const int tok = t0 + c * kC, len = min(kC, t1 - tok);
-    const uint16_t* kt = ktb + size_t(c) * p.Hk * (kD * kC);
-    const uint16_t* tri = trib + size_t(c) * p.Hv * kTriElems;
-    const float* co = cob + size_t(c) * p.Hv * kCoefs;
-    const bool rok = 16 * w + l16 < len;
-    const int64_t rt = tok + (rok ? 16 * w + l16 : 0);
-    bf16x8 kf[4], qf[4];
-    load_rows(kf, p.k + rt * p.k_t + hk * p.k_h + 8 * g4, rok);
-    f32x4 v[CT];
-    const int tr = 16 * w + 4 * g4;  // this lane's four token rows
+      for (int i = 0; i < 4; ++i) S[r][i] = bf16_to_f32(static_cast<const uint16_t*>(p.s0)[state_at(r, i)]);
+  } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool ok = tr + i < len;
-      const uint16_t* vp = p.v + int64_t(tok + (ok ? tr + i : 0)) * p.v_t + h * p.v_h + col0 + l16;
+    for (int r = 0; r < 8; ++r)
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) v[ct][i] = ok ? bf16_to_f32(vp[16 * ct]) : 0.f;
-    }
-    const f32x4 cb = *reinterpret_cast<const f32x4*>(co + kBeta * kC + tr);
-    const f32x4 ck = *reinterpret_cast<const f32x4*>(co + kKs * kC + tr);
-    const f32x4 cq = *reinterpret_cast<const f32x4*>(co + kQs * kC + tr);
-    const f32x4 cu = *reinterpret_cast<const f32x4*>(co + kUs * kC + tr);
-    const float end = co[kEnd * kC];
-    bf16x8 tf[2][NP], pf[2][NP], ktf[2][2];
-    load_rows(qf, p.q + rt * p.q_t + hk * p.q_h + 8 * g4, rok);
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const size_t u = (size_t(unit_of(w, min(s, steps - 1))) * NP + i) * kUnit;
-        tf[s][i] = *reinterpret_cast<const bf16x8*>(tri + u);
-        pf[s][i] = *reinterpret_cast<const bf16x8*>(tri + kUnits * kMaxPieces * kUnit + u);
-      }
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) ktf[r][s] = *reinterpret_cast<const bf16x8*>(kt + (4 * w + 2 * r + s) * kUnit);
-
-    // the state's pieces
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) put4<NP>(L.S, 16 * ct + l16, 32 * w + 16 * r + 4 * g4, S[r][ct]);
-    __syncthreads();
-    // K S and Q S, rows of token tile w
-    f32x4 ks[CT] = {}, qs[CT] = {};
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int b = 0; b < NP; ++b) {
-          const bf16x8 f = *reinterpret_cast<const bf16x8*>(&L.S[b][16 * ct + l16][32 * s + 8 * g4]);
-          ks[ct] = mfma32(kf[s], f, ks[ct]);
-          qs[ct] = mfma32(qf[s], f, qs[ct]);
-        }
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) put4<NP>(L.R, 16 * ct + l16, tr, cb * v[ct] - ck * ks[ct]);
-    __syncthreads();
-    f32x4 u[CT] = {};
-    tri_mul<NP, CT>(u, tf, L.R, steps, l16, g4);
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      put4<NP>(L.U, 16 * ct + l16, tr, u[ct]);
-      put4<NP>(L.W, 16 * ct + l16, tr, cu * u[ct]);
-    }
-    __syncthreads();
-    // the state's update, key rows 32 w ..
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) S[r][ct] *= end;
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int b = 0; b < NP; ++b) {
-          const bf16x8 f = *reinterpret_cast<const bf16x8*>(&L.W[b][16 * ct + l16][32 * s + 8 * g4]);
-#pragma unroll
-          for (int r = 0; r < 2; ++r) S[r][ct] = mfma32(ktf[r][s], f, S[r][ct]);
-        }
-    // the outputs
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) qs[ct] *= cq;
-    tri_mul<NP, CT>(qs, pf, L.U, steps, l16, g4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (tr + i < len) {
-        uint16_t* o = p.out + int64_t(tok + tr + i) * p.o_t + h * p.o_h + col0 + l16;
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) o[16 * ct] = f32_to_bf16(qs[ct][i]);
-      }
-    }
+      for (int i = 0; i < 4; ++i) S[r][i] = static_cast<const float*>(p.s0)[state_at(r, i)];
   }
+
+  const int64_t slot0 = first_slot(p, n);
+  const char* headb = p.ws + lay.head + (size_t(slot0) * p.Hk + hk) * (kHeadUnits * 1024);
+  const char* trib = p.ws + lay.tri + (size_t(slot0) * p.Hv + h) * (kMaxTri * 1024);
+  const char* cob = p.ws + lay.coef + (size_t(slot0) * p.Hv + h) * (kCoefs * 4);
+  const char* vb = reinterpret_cast<const char*>(p.v + int64_t(t0) * p.v_t + h * p.v_h);
+  char* ob = reinterpret_cast<char*>(p.out + int64_t(t0) * p.o_t + h * p.o_h);
+  // in bytes: the strides, and where this lane's column of its first row is
+  const uint32_t v_t = 2 * uint32_t(p.v_t), o_t = 2 * uint32_t(p.o_t);
+  const uint32_t v_lane = 4 * g4 * v_t + 2 * col, o_lane = 4 * g4 * o_t + 2 * col;
+
+  const auto fetch = [&](int c, Stage<NP>& d) __attribute__((always_inline)) {
+    const __amdgpu_buffer_rsrc_t head = rsrc_of(headb + size_t(c) * p.Hk * (kHeadUnits * 1024));
+    const __amdgpu_buffer_rsrc_t tri = rsrc_of(trib + size_t(c) * p.Hv * (kMaxTri * 1024));
+    const __amdgpu_buffer_rsrc_t co = rsrc_of(cob + size_t(c) * p.Hv * (kCoefs * 4));
+    const int lane16 = lane * 16;
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+    for (int i = 0; i < kHeadUnits / W; ++i) load_lds(head, (w + W * i) * 1024, &d.unit[w + W * i][0], lane16);
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
+    for (int i = 0; i < (Stage<NP>::kTri + W - 1) / W; ++i) {
+      const int u = min(w + W * i, Stage<NP>::kTri - 1);  // (the last one more than once)
+      load_lds(tri, u * 1024, &d.unit[kHeadUnits + u][0], lane16);
+    }
+    load_lds(co, (w & 1) * 1024, &d.coef[64 * (w & 1)], w & 1 ? min(lane16, kCoefs * 4 - 1024 - 16) : lane16);
+  };
+  // The chunk's values in this lane's column.  Rows behind the sequence's end are
+  // zeros, or rows of it where rows overlap: their coefficients are 0.
+  uint32_t v[4][4];
+  const auto fetch_values = [&](int c) __attribute__((always_inline)) {
+    c = min(c, nc - 1);
+    uint32_t row = v_t;
+    asm("" : "+s"(row));  // (16 multiples of it are not worth 16 registers)
+    const uint32_t last = uint32_t(min(kC, t1 - t0 - c * kC) - 1);
+    const __amdgpu_buffer_rsrc_t vc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(vb + int64_t(c) * kC * p.v_t * 2), 0, int(last * v_t + 2 * kD), kRsrcWord3);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const size_t e = sbase + size_t(32 * w + 16 * r + 4 * g4 + i) * kD + 16 * ct;
-        if (p.state_bf16)
-          static_cast<uint16_t*>(p.sT)[e] = f32_to_bf16(S[r][ct][i]);
-        else
-          static_cast<float*>(p.sT)[e] = S[r][ct][i];
+    for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[rt][i] = __builtin_amdgcn_raw_buffer_load_b16(vc, int(v_lane + uint32_t(16 * rt + i) * row), 0, 0);
+  };
+  if (nc > 0) {
+    fetch(0, L[0]);
+    fetch_values(0);
+  }
+  __builtin_amdgcn_s_waitcnt(kVmcnt0);
+  __syncthreads();
+  const auto step = [&](int c, const Stage<NP>& d, Stage<NP>& dn, auto whole) __attribute__((always_inline)) {
+    // one register for the units' base (the second stage lies past the offsets that an LDS access holds)
+    typedef const __attribute__((address_space(3))) char* lds_t;
+    lds_t ub = (lds_t)(&d.unit[0][lane]), cb0 = (lds_t)(&d.coef[g4]);
+    asm("" : "+v"(ub));
+    asm("" : "+v"(cb0));
+    const auto op = [&](int u) { return *reinterpret_cast<const __attribute__((address_space(3))) f16x8*>(ub + u * 1024); };
+    const auto coef = [&](int k, int rt) {
+      return *reinterpret_cast<const __attribute__((address_space(3))) f32x4*>(cb0 + (k * (kC / 4) + 4 * rt) * 16);
+    };
+    // (unconditional: the waits for values count the loads behind them)
+    if (whole()) fetch(min(c + 1, nc - 1), dn);
+    // Bring the larger of |S| and |v| in the column to [2^7, 2^8) (zeros and the smallest columns
+    // are left below), unless it is between 2^3 and there in every column of the wave.
+    {
+      float ms = 0.f, mv = 0.f;
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ms = fmaxf(ms, fabsf(S[r][i]));
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mv = fmaxf(mv, fabsf(bf16_lo(v[rt][i])));
+      const float big = over_column(fmaxf(ms * inv, mv));
+      const uint32_t e = __float_as_uint(big) >> 23, now = max(e, 27u) - 7u, old = __float_as_uint(inv) >> 23;
+      if (__any(now > old || now + 4 < old)) {
+        sc = __uint_as_float((254u - now) << 23);
+        const float ratio = sc * inv;
+        inv = __uint_as_float(now << 23);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) S[r] *= ratio;
       }
+    }
+    // K S and Q S
+    f32x4 ks[4] = {}, qs[4] = {};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      f16x4 lo[NP], hi[NP];
+      f16x8 b[NP];
+      cut4<NP>(S[2 * s], lo);
+      cut4<NP>(S[2 * s + 1], hi);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) b[i] = cath(lo[i], hi[i]);
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) {
+        const f16x8 k = op(4 * rt + s), q = op(kKUnits + 4 * rt + s);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) ks[rt] = mfma32h(k, b[i], ks[rt]);
+        qs[rt] = mfma32h(q, b[0], qs[rt]);
+      }
+    }
+    // R = beta V - beta e^G K~ S, and U = T R
+    f16x4 r[4][NP];
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+      const f32x4 cb = coef(kBeta, rt), ck = coef(kKs, rt);
+      f32x4 x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = (cb[i] * sc) * bf16_lo(v[rt][i]) - ck[i] * ks[rt][i];
+      cut4<NP>(x, r[rt]);
+    }
+    if (whole()) fetch_values(c + 1);
+    f32x4 u[4] = {};
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+      for (int z = 0; z <= rt / 2; ++z)
+#pragma unroll
+        for (int a = 0; a < NP; ++a) {
+          const f16x8 t = op(kHeadUnits + unit_of(rt, z) * NP + a);
+#pragma unroll
+          for (int b = 0; a + b < NP; ++b) u[rt] = mfma32h(t, cath(r[2 * z][b], r[2 * z + 1][b]), u[rt]);
+        }
+    // the state's update with W = rk e^(G_C - G) U
+    const float end = coef(kEnd, 0)[0];
+    f16x4 up[4];
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+      cut4<1>(u[rt], &up[rt]);
+      cut4<NP>(coef(kUs, rt) * u[rt], r[rt]);
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      S[t] *= end;
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const f16x8 k = op(2 * kKUnits + 2 * t + z);
+#pragma unroll
+        for (int b = 0; b < NP; ++b) S[t] = mfma32h(k, cath(r[2 * z][b], r[2 * z + 1][b]), S[t]);
+      }
+    }
+    // out = scale (e^G Q~ S + P U)
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+      qs[rt] *= coef(kQs, rt);
+#pragma unroll
+      for (int z = 0; z <= rt / 2; ++z)
+        qs[rt] = mfma32h(op(kHeadUnits + kUnits * NP + unit_of(rt, z)), cath(up[2 * z], up[2 * z + 1]), qs[rt]);
+      qs[rt] *= p.scale * inv;
+    }
+    char* oc = ob + int64_t(c) * kC * p.o_t * 2;
+    uint32_t orow = o_t;
+    asm("" : "+s"(orow));
+    const auto store = [&](int rt, int i) __attribute__((always_inline)) {
+      *reinterpret_cast<bf16*>(oc + uint64_t(16 * rt + i) * orow + o_lane) = (bf16)qs[rt][i];
+    };
+    if (whole()) {
+      // This wave's loads of the next chunk into LDS have to be there before the
+      // barrier, its stores need not: these 16 are its last accesses to memory
+      // (nothing is scheduled across the lines around them).
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store(rt, i);
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(kVmcnt16);
+      __syncthreads();
+    } else {
+      const int len = t1 - t0 - c * kC;
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (16 * rt + 4 * g4 + i < len) store(rt, i);
+    }
+  };
+  // whole chunks, then the rest
+  const int full = (t1 - t0) / kC;
+  for (int c = 0; c < full; c += 2) {
+    step(c, L[0], L[1], std::true_type{});
+    if (c + 1 < full) step(c + 1, L[1], L[0], std::true_type{});
+  }
+  if (full < nc) step(full, L[full & 1], L[0], std::false_type{});
+#pragma unroll
+  for (int r = 0; r < 8; ++r) S[r] *= inv;
+  if (p.state_bf16) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) static_cast<uint16_t*>(p.sT)[state_at(r, i)] = f32_to_bf16(S[r][i]);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) static_cast<float*>(p.sT)[state_at(r, i)] = S[r][i];
+  }
 }
 
 template <int NP>
@@ -462,11 +623,15 @@ hipError_t launch(const GdrParams& p, int cus, hipStream_t st) {
       e != hipSuccess)
     return e;
   const int64_t pairs = int64_t(p.N) * p.Hv;
-  if (pairs * 4 >= cus)
-    return hipLaunchKernel(reinterpret_cast<const void*>(&scan_kernel<NP, 2>), dim3(uint32_t(pairs * 4)),
-                           dim3(256), args, 0, st);
-  return hipLaunchKernel(reinterpret_cast<const void*>(&scan_kernel<NP, 1>), dim3(uint32_t(pairs * 8)),
-                         dim3(256), args, 0, st);
+  // A workgroup fills a compute unit's LDS, so with at most half as many states
+  // as units two workgroups of 64 columns each take one: 8 x 2048 tokens, 16
+  // heads 129 us against 155, 1 x 8192, 8 heads 280 against 366; above that one
+  // of 128 columns and two waves per SIMD: 32 ragged prompts, 32 heads 326
+  // against 417.
+  const bool two = 2 * pairs <= cus;
+  return hipLaunchKernel(two ? reinterpret_cast<const void*>(&scan_kernel<NP, 4>)
+                             : reinterpret_cast<const void*>(&scan_kernel<NP, 8>),
+                         dim3(uint32_t(pairs * (two ? 2 : 1))), dim3(two ? 256 : 512), args, 0, st);
 }
 
 }  // namespace
@@ -475,15 +640,15 @@ GdrLayout gdr_layout(int64_t T, int Hk, int Hv, int64_t N) {
   GdrLayout l{};
   l.slots = T / kC + N;
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  l.kt = 0;
-  l.tri = l.kt + up(size_t(l.slots) * Hk * kD * kC * 2);
-  l.coef = l.tri + up(size_t(l.slots) * Hv * kTriElems * 2);
+  l.head = 0;
+  l.tri = l.head + up(size_t(l.slots) * Hk * kHeadUnits * 1024);
+  l.coef = l.tri + up(size_t(l.slots) * Hv * kMaxTri * 1024);
   l.total = l.coef + up(size_t(l.slots) * Hv * kCoefs * 4);
   return l;
 }
 
 hipError_t launch_gdr_chunked(const GdrParams& p, int cus, hipStream_t stream) {
-  return p.state_bf16 ? launch<2>(p, cus, stream) : launch<3>(p, cus, stream);
+  return p.state_bf16 ? launch<1>(p, cus, stream) : launch<2>(p, cus, stream);
 }
 
 }  // namespace kda

@@ -43,12 +43,14 @@ kda_status_t gdr_checks(const void* q, const void* k, const void* v, const void*
     if (misaligned(p, 16)) return KDA_ERR_INVALID_ARG;
   if (misaligned(a, 2) || misaligned(beta, 2) || misaligned(A_log, 4) || misaligned(dt_bias, 4))
     return KDA_ERR_INVALID_ARG;
-  // 2^31 tokens of at most 2^30 elements: byte offsets below 2^62
-  constexpr int64_t kMaxStride = int64_t(1) << 30;
-  for (int64_t x : {s.q_token, s.q_head, s.k_token, s.k_head, s.v_token, s.v_head, s.out_token, s.out_head})
-    if (x < 0 || x % 8 || x > kMaxStride) return KDA_ERR_INVALID_ARG;
+  // token strides: 32-bit byte offsets over the 64 rows of a chunk
+  constexpr int64_t kMaxHead = int64_t(1) << 30, kMaxToken = int64_t(1) << 24;
+  for (int64_t x : {s.q_token, s.k_token, s.v_token, s.out_token})
+    if (x < 0 || x % 8 || x > kMaxToken) return KDA_ERR_INVALID_ARG;
+  for (int64_t x : {s.q_head, s.k_head, s.v_head, s.out_head})
+    if (x < 0 || x % 8 || x > kMaxHead) return KDA_ERR_INVALID_ARG;
   for (int64_t x : {s.a_token, s.a_head, s.beta_token, s.beta_head})
-    if (x < 0 || x > kMaxStride) return KDA_ERR_INVALID_ARG;
+    if (x < 0 || x > kMaxHead) return KDA_ERR_INVALID_ARG;
   if ((rows > 1 && s.out_token == 0) || (hv > 1 && s.out_head == 0)) return KDA_ERR_INVALID_ARG;
   return KDA_OK;
 }

@@ -37,7 +37,7 @@ struct GdrParams {
 // cover every batch of N sequences and T tokens.
 struct GdrLayout {
   int64_t slots;
-  size_t kt, tri, coef, total;  // byte offsets of the parts, and their sum
+  size_t head, tri, coef, total;  // byte offsets of the parts, and their sum
 };
 GdrLayout gdr_layout(int64_t T, int Hk, int Hv, int64_t N);
 

@@ -91,13 +91,15 @@ size_t kda_gdr_get_workspace_size(int64_t max_tokens, int32_t key_heads, int32_t
  * q, k, v and out are 16-byte aligned, the states 16-byte, a and beta_logits
  * 2-byte.  value_heads is a multiple of key_heads, at most 65536;
  * num_seqs * value_heads < 2^21; (num_tokens / 64 + num_seqs) * value_heads <
- * 2^24; strides at most 2^30.  q, k, v, a, beta_logits
+ * 2^24; token strides of q, k, v and out at most 2^24, other strides 2^30.  q, k, v, a, beta_logits
  * and out may be NULL when num_tokens is 0, workspace too when the size query
  * gives 0.
  *
  * Numerics.  Sums, decays and the state are fp32 (sums of log decays fp64).
- * With an fp32 state every factor of a matrix product keeps 24 bits, with a
- * bf16 state 16 bits; the final state and out are rounded once, at the end.
+ * Factors of matrix products keep 22 bits with an fp32 state and 11 bits with
+ * a bf16 state (out, which is bf16, 11 bits either way), relative to the
+ * largest element of their column: finite values and states of any size are
+ * taken.  The final state and out are rounded once, at the end.
  * An input that is not finite makes the rows of its sequence and head from
  * its chunk of 64 tokens on, and their final state, undefined; other
  * sequences and heads are not affected.
