@@ -495,18 +495,22 @@ def _refuse(t, name, dtype, shape, index):
 
 def _view(t, name, dtype, shape, index):
     """Device pointer of t, whose strides are the caller's to look at."""
-    if not (isinstance(t, _torch_module.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.get_device() == index):
-        _refuse(t, name, dtype, shape, index)
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, index)
 
 
 def _on(t, name, dtype, shape, index):
     """Device pointer of t: dense, of this dtype and shape, on GPU `index`."""
-    if not (isinstance(t, _torch_module.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.get_device() == index and t.is_contiguous()):
-        _refuse(t, name, dtype, shape, index)
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, index)
 
 
 def _gpu(t, name):
@@ -520,15 +524,14 @@ def _gpu(t, name):
 
 def _call(name, fn, index, stream, before, after):
     """fn(*before, stream, *after) on GPU `index`; raises on a refusal."""
-    cuda = _torch_module.cuda
     if stream is None:
         stream = _torch_module._C._cuda_getCurrentRawStream(index)
-    elif isinstance(stream, cuda.Stream):
+    elif isinstance(stream, _torch_module.cuda.Stream):
         stream = stream.cuda_stream
-    if index == cuda.current_device():
+    if index == _torch_module._C._cuda_getDevice():
         rc = fn(*before, stream, *after)
     else:
-        with cuda.device(index):
+        with _torch_module.cuda.device(index):
             rc = fn(*before, stream, *after)
     if rc != KDA_OK:
         detail = kda_last_hip_error() if rc == 4 else ""
@@ -546,12 +549,20 @@ def _state_dtype(t):
 
 
 @functools.lru_cache(maxsize=256)
-def _gdr_strides(*strides):
-    return _GdrStrides(*strides)
+def _gdr_strides(one_row, one_key_head, one_value_head, q, k, v, a, beta_logits, out):
+    """kda_gdr_strides_t of tensors with these strides (0 for a dimension of one
+    element, whose stride means nothing); None where channels are not adjacent."""
+    if any(st[2] != 1 for st in (q, k, v, out)):
+        return None
+    flat = []
+    for st, one_head in ((q, one_key_head), (k, one_key_head), (v, one_value_head),
+                         (a, one_value_head), (beta_logits, one_value_head), (out, one_value_head)):
+        flat += [0 if one_row else st[0], 0 if one_head else st[1]]
+    return _GdrStrides(*flat)
 
 
 def _gdr_rows(q, k, v, a, beta_logits, A_log, dt_bias, out):
-    """(pointers of the inputs, pointer of out, GPU, rows, key heads, value heads, strides or None)."""
+    """(pointers of the inputs, pointer of out, GPU, rows, key heads, value heads, strides)."""
     dev = _gpu(q, "q")
     torch = _torch_module
     bf, f32 = torch.bfloat16, torch.float32
@@ -566,13 +577,10 @@ def _gdr_rows(q, k, v, a, beta_logits, A_log, dt_bias, out):
             _view(a, "a", bf, gates, dev), _view(beta_logits, "beta_logits", bf, gates, dev),
             _on(A_log, "A_log", f32, per_head, dev), _on(dt_bias, "dt_bias", f32, per_head, dev))
     o = _view(out, "out", bf, heads, dev)
-    st = None
-    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and a.is_contiguous()
-            and beta_logits.is_contiguous() and out.is_contiguous()):
-        sq, sk, sv, so = q.stride(), k.stride(), v.stride(), out.stride()
-        if not sq[2] == sk[2] == sv[2] == so[2] == 1:
-            raise ValueError("q, k, v and out must have contiguous channels")
-        st = _gdr_strides(*sq[:2], *sk[:2], *sv[:2], *a.stride(), *beta_logits.stride(), *so[:2])
+    st = _gdr_strides(T <= 1, hk == 1, hv == 1, q.stride(), k.stride(), v.stride(), a.stride(),
+                      beta_logits.stride(), out.stride())
+    if st is None:
+        raise ValueError("q, k, v and out must have contiguous channels")
     return ptrs, o, dev, T, hk, hv, st
 
 

@@ -8,12 +8,20 @@
 //   o = scale (a y + (q~ . k~) u),  S <- a S + k~ u^T
 // (o from the old state, so that k and q share one reduction and one barrier).
 // A decode step is bound by the state's bytes, read and written once: every
-// load of the state is issued before anything else, 16 bytes per lane, 64 KB
-// (fp32) in flight per workgroup at V = 128.
+// load of the state is issued before anything else, 16 bytes per lane, 32 KB in
+// flight per workgroup.  256 sequences x 16 heads, fp32: 108.6 us, 5.0 TB/s (a
+// copy reaches 5.1).
 #include "kda_gdr.h"
 
 namespace kda {
 namespace {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// two numbers rounded to bf16 (one instruction; NaN stays NaN)
+__device__ __forceinline__ uint32_t round2(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
 
 template <bool BF16, int V>
 __global__ __launch_bounds__(256) void serial_kernel(GdrParams p) {
@@ -129,18 +137,18 @@ __global__ __launch_bounds__(256) void serial_kernel(GdrParams p) {
     if (tid < TPR) {
       uint16_t* o = p.out + t * p.o_t + h * p.o_h + col;
       if (BF16)
-        *reinterpret_cast<uint4*>(o) = uint4{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                             pack_bf16x2(y[E - 4], y[E - 3]), pack_bf16x2(y[E - 2], y[E - 1])};
+        *reinterpret_cast<uint4*>(o) = uint4{round2(y[0], y[1]), round2(y[2], y[3]),
+                                             round2(y[E - 4], y[E - 3]), round2(y[E - 2], y[E - 1])};
       else
-        *reinterpret_cast<uint2*>(o) = uint2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+        *reinterpret_cast<uint2*>(o) = uint2{round2(y[0], y[1]), round2(y[2], y[3])};
     }
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     if (BF16)
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.sT) + base + r * kD) =
-          uint4{pack_bf16x2(s[r][0], s[r][1]), pack_bf16x2(s[r][2], s[r][3]),
-                pack_bf16x2(s[r][E - 4], s[r][E - 3]), pack_bf16x2(s[r][E - 2], s[r][E - 1])};
+          uint4{round2(s[r][0], s[r][1]), round2(s[r][2], s[r][3]),
+                round2(s[r][E - 4], s[r][E - 3]), round2(s[r][E - 2], s[r][E - 1])};
     else
       *reinterpret_cast<f32x4*>(static_cast<float*>(p.sT) + base + r * kD) =
           f32x4{s[r][0], s[r][1], s[r][2], s[r][3]};
@@ -149,16 +157,21 @@ __global__ __launch_bounds__(256) void serial_kernel(GdrParams p) {
 
 }  // namespace
 
-hipError_t launch_gdr_serial(const GdrParams& p, int cus, hipStream_t stream) {
+hipError_t launch_gdr_serial(const GdrParams& p, hipStream_t stream) {
   GdrParams arg = p;
   void* args[] = {&arg};
   const int64_t pairs = int64_t(p.N) * p.Hv;
-  const bool split = pairs < 2 * cus;
-  const void* f = split ? (p.state_bf16 ? reinterpret_cast<const void*>(&serial_kernel<true, 32>)
-                                        : reinterpret_cast<const void*>(&serial_kernel<false, 32>))
-                        : (p.state_bf16 ? reinterpret_cast<const void*>(&serial_kernel<true, 128>)
-                                        : reinterpret_cast<const void*>(&serial_kernel<false, 128>));
-  return hipLaunchKernel(f, dim3(uint32_t(pairs * (split ? 4 : 1))), dim3(256), args, 0, stream);
+  // Columns per workgroup: few states are spread over more workgroups (1 x 16:
+  // 4.2 us with 32 columns, 4.9 with 128), a bf16 state of 64 columns is too
+  // little for one (128 x 32: 60 us against 57 with 128; fp32 256 x 16: 108.6
+  // against 110.8).
+  const int cols = pairs <= 64 ? 32 : p.state_bf16 && pairs >= 512 ? 128 : 64;
+  const void* f = cols == 32   ? (p.state_bf16 ? reinterpret_cast<const void*>(&serial_kernel<true, 32>)
+                                               : reinterpret_cast<const void*>(&serial_kernel<false, 32>))
+                  : cols == 64 ? (p.state_bf16 ? reinterpret_cast<const void*>(&serial_kernel<true, 64>)
+                                               : reinterpret_cast<const void*>(&serial_kernel<false, 64>))
+                               : reinterpret_cast<const void*>(&serial_kernel<true, 128>);
+  return hipLaunchKernel(f, dim3(uint32_t(pairs * (kD / cols))), dim3(256), args, 0, stream);
 }
 
 }  // namespace kda

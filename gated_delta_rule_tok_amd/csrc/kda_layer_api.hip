@@ -127,15 +127,15 @@ kda_status_t kda_gdr_prefill_fwd(const void* q, const void* k, const void* v, co
   p.T = int(num_tokens);
   p.N = num_seqs;
   p.ws = static_cast<char*>(workspace);
-  int cus = 0;
-  if (hipError_t e = kda::device_cus(&cus); e != hipSuccess) return failed(e, "device query");
   hipStream_t st = static_cast<hipStream_t>(stream);
   // a few tokens per sequence: token after token, as kda_chunk_prefill_fwd does
   if (num_tokens <= int64_t(kda::kDecodeTokensPerSeq) * num_seqs) {
-    if (hipError_t e = kda::launch_gdr_serial(p, cus, st); e != hipSuccess)
+    if (hipError_t e = kda::launch_gdr_serial(p, st); e != hipSuccess)
       return failed(e, "serial delta rule launch");
     return KDA_OK;
   }
+  int cus = 0;
+  if (hipError_t e = kda::device_cus(&cus); e != hipSuccess) return failed(e, "device query");
   if (hipError_t e = kda::launch_gdr_chunked(p, cus, st); e != hipSuccess)
     return failed(e, "chunked delta rule launch");
   return KDA_OK;
@@ -166,9 +166,7 @@ kda_status_t kda_gdr_decode_step(const void* q, const void* k, const void* v, co
   p.slots = num_slots;
   p.T = num_seqs;
   p.N = num_seqs;
-  int cus = 0;
-  if (hipError_t e = kda::device_cus(&cus); e != hipSuccess) return failed(e, "device query");
-  if (hipError_t e = kda::launch_gdr_serial(p, cus, static_cast<hipStream_t>(stream)); e != hipSuccess)
+  if (hipError_t e = kda::launch_gdr_serial(p, static_cast<hipStream_t>(stream)); e != hipSuccess)
     return failed(e, "serial delta rule launch");
   return KDA_OK;
 }
