@@ -29,6 +29,7 @@
 //    (the map is a contraction), hence |U| <= (1 + sqrt(128) + 64) 2^8 < 2^15:
 //    no finite input overflows, and what fp16 loses below 2^-14 is under 2^-32
 //    of the column's largest element.  T and P are at most 1.
+#include <algorithm>
 #include <type_traits>
 
 #include "kda_gdr.h"
@@ -340,6 +341,14 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(GdrParams p, GdrLayout lay
 
 // ---- scan -------------------------------------------------------------------
 //
+// Three kinds of it.  kWhole: whole sequences.  With few states and long
+// sequences most of the machine would idle, so there sequences are cut into
+// segments (kda_segment.hip has the table and the combine): a segment maps the
+// state S entering it to P S + R, and kSummary forms R (from zeros) and P (from
+// the identity, with values 0) as 256 columns, of all segments but a sequence's
+// last at once, without outputs; after the combine kRerun walks all segments at
+// once, each from its state.
+//
 // A wave owns 16 value columns of one state for the whole sequence and
 // needs nothing of the other waves' columns: S, R and U stay in its registers
 // from the accumulators of one product to the operands of the next, without
@@ -381,19 +390,35 @@ __device__ __forceinline__ float over_column(float m) {
   return fmaxf(m, __shfl_xor(m, 32));
 }
 
-template <int NP, int W>
+enum { kWhole, kSummary, kRerun };
+
+template <int NP, int W, int KIND>
 __global__ __launch_bounds__(64 * W, W / 4) void scan_kernel(GdrParams p, GdrLayout lay) {
   __shared__ Stage<NP> L[2];
-  constexpr int kSlices = kD / (16 * W);
+  constexpr int kSlices = (KIND == kSummary ? 2 : 1) * kD / (16 * W);
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int group = p.Hv / p.Hk;
   // the value heads of a key head on one XCD: its units of K and Q are in that L2
   const int item = work_item(blockIdx.x, gridDim.x, kSlices * group);
-  const int n = item / (kSlices * p.Hv), h = item / kSlices % p.Hv, hk = h / group;
-  const int col = (item % kSlices * W + w) * 16 + l16;  // this lane's value column
-  int t0, t1;
-  gdr_range(p, n, t0, t1);
+  const int m = item / (kSlices * p.Hv), h = item / kSlices % p.Hv, hk = h / group;
+  const int col = ((item % kSlices * W + w) * 16 + l16) % kD;  // this lane's value column
+  const bool map = KIND == kSummary && item % kSlices >= kSlices / 2;  // a column of P
+  int n = m, t0, t1;
+  bool last = true;
+  int64_t slot0;
+  if (KIND == kWhole) {
+    gdr_range(p, n, t0, t1);
+    slot0 = first_slot(p, n);
+  } else {
+    const int4 e = *reinterpret_cast<const int4*>(p.seg + 4 * m);
+    n = e.x;
+    last = e.w & 1;
+    if (n < 0 || (KIND == kSummary && last)) return;
+    t0 = e.y;
+    t1 = e.z;
+    slot0 = first_slot(p, n) + (t0 - min(max(p.cu[n], 0), p.T)) / kC;
+  }
   const int nc = (t1 - t0 + kC - 1) / kC;
 
   f32x4 S[8];                // the column's state times sc
@@ -402,7 +427,18 @@ __global__ __launch_bounds__(64 * W, W / 4) void scan_kernel(GdrParams p, GdrLay
   const auto state_at = [&](int r, int i) {
     return sbase + size_t(32 * (r >> 1) + 8 * g4 + 4 * (r & 1) + i) * kD;
   };
-  if (!p.s0) {
+  if (KIND == kSummary) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[r][i] = map && 32 * (r >> 1) + 8 * g4 + 4 * (r & 1) + i == col ? 1.f : 0.f;
+  } else if (KIND == kRerun) {
+    const float* s0 = p.starts + (size_t(m) * p.Hv + h) * (kD * kD) + col;
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[r][i] = s0[state_at(r, i) - sbase];
+  } else if (!p.s0) {
 #pragma unroll
     for (int r = 0; r < 8; ++r) S[r] = f32x4{};
   } else if (p.state_bf16) {
@@ -417,7 +453,6 @@ __global__ __launch_bounds__(64 * W, W / 4) void scan_kernel(GdrParams p, GdrLay
       for (int i = 0; i < 4; ++i) S[r][i] = static_cast<const float*>(p.s0)[state_at(r, i)];
   }
 
-  const int64_t slot0 = first_slot(p, n);
   const char* headb = p.ws + lay.head + (size_t(slot0) * p.Hk + hk) * (kHeadUnits * 1024);
   const char* trib = p.ws + lay.tri + (size_t(slot0) * p.Hv + h) * (kMaxTri * 1024);
   const char* cob = p.ws + lay.coef + (size_t(slot0) * p.Hv + h) * (kCoefs * 4);
@@ -433,24 +468,29 @@ __global__ __launch_bounds__(64 * W, W / 4) void scan_kernel(GdrParams p, GdrLay
     const __amdgpu_buffer_rsrc_t co = rsrc_of(cob + size_t(c) * p.Hv * (kCoefs * 4));
     const int lane16 = lane * 16;
 #pragma unroll
-    for (int i = 0; i < kHeadUnits / W; ++i) load_lds(head, (w + W * i) * 1024, &d.unit[w + W * i][0], lane16);
+    for (int i = 0; i < kHeadUnits / W; ++i) {
+      if (KIND == kSummary && W * i >= kKUnits && W * i < 2 * kKUnits) continue;  // Q
+      load_lds(head, (w + W * i) * 1024, &d.unit[w + W * i][0], lane16);
+    }
+    constexpr int kTri = KIND == kSummary ? kUnits * NP : Stage<NP>::kTri;
 #pragma unroll
-    for (int i = 0; i < (Stage<NP>::kTri + W - 1) / W; ++i) {
-      const int u = min(w + W * i, Stage<NP>::kTri - 1);  // (the last one more than once)
+    for (int i = 0; i < (kTri + W - 1) / W; ++i) {
+      const int u = min(w + W * i, kTri - 1);  // (the last one more than once)
       load_lds(tri, u * 1024, &d.unit[kHeadUnits + u][0], lane16);
     }
     load_lds(co, (w & 1) * 1024, &d.coef[64 * (w & 1)], w & 1 ? min(lane16, kCoefs * 4 - 1024 - 16) : lane16);
   };
   // The chunk's values in this lane's column.  Rows behind the sequence's end are
-  // zeros, or rows of it where rows overlap: their coefficients are 0.
+  // zeros, or rows of it where rows overlap: their coefficients are 0.  (No row
+  // is inside the buffer for a column of P.)
   uint32_t v[4][4];
   const auto fetch_values = [&](int c) __attribute__((always_inline)) {
     c = min(c, nc - 1);
     uint32_t row = v_t;
     asm("" : "+s"(row));  // (16 multiples of it are not worth 16 registers)
-    const uint32_t last = uint32_t(min(kC, t1 - t0 - c * kC) - 1);
+    const uint32_t end = uint32_t(min(kC, t1 - t0 - c * kC) - 1);
     const __amdgpu_buffer_rsrc_t vc = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(vb + int64_t(c) * kC * p.v_t * 2), 0, int(last * v_t + 2 * kD), kRsrcWord3);
+        const_cast<char*>(vb + int64_t(c) * kC * p.v_t * 2), 0, map ? 0 : int(end * v_t + 2 * kD), kRsrcWord3);
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
@@ -512,7 +552,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void scan_kernel(GdrParams p, GdrLay
         const f16x8 k = op(4 * rt + s), q = op(kKUnits + 4 * rt + s);
 #pragma unroll
         for (int i = 0; i < NP; ++i) ks[rt] = mfma32h(k, b[i], ks[rt]);
-        qs[rt] = mfma32h(q, b[0], qs[rt]);
+        if (KIND != kSummary) qs[rt] = mfma32h(q, b[0], qs[rt]);
       }
     }
     // R = beta V - beta e^G K~ S, and U = T R
@@ -554,6 +594,11 @@ __global__ __launch_bounds__(64 * W, W / 4) void scan_kernel(GdrParams p, GdrLay
 #pragma unroll
         for (int b = 0; b < NP; ++b) S[t] = mfma32h(k, cath(r[2 * z][b], r[2 * z + 1][b]), S[t]);
       }
+    }
+    if (KIND == kSummary) {
+      __builtin_amdgcn_s_waitcnt(kVmcnt0);
+      __syncthreads();
+      return;
     }
     // out = scale (e^G Q~ S + P U)
 #pragma unroll
@@ -600,7 +645,15 @@ __global__ __launch_bounds__(64 * W, W / 4) void scan_kernel(GdrParams p, GdrLay
   if (full < nc) step(full, L[full & 1], L[0], std::false_type{});
 #pragma unroll
   for (int r = 0; r < 8; ++r) S[r] *= inv;
-  if (p.state_bf16) {
+  if (KIND == kSummary) {
+    float* out = p.summ + ((size_t(m) * p.Hv + h) * 2 + map) * (kD * kD) + col;
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[state_at(r, i) - sbase] = S[r][i];
+  } else if (!last) {
+    return;
+  } else if (p.state_bf16) {
 #pragma unroll
     for (int r = 0; r < 8; ++r)
 #pragma unroll
@@ -613,25 +666,79 @@ __global__ __launch_bounds__(64 * W, W / 4) void scan_kernel(GdrParams p, GdrLay
   }
 }
 
-template <int NP>
-hipError_t launch(const GdrParams& p, int cus, hipStream_t st) {
+// ---- launches -----------------------------------------------------------------
+
+template <int NP, int W, int KIND>
+hipError_t launch_scan(const GdrParams& p, GdrLayout lay, int64_t seqs, hipStream_t st) {
   GdrParams arg = p;
-  GdrLayout lay = gdr_layout(p.T, p.Hk, p.Hv, p.N);
   void* args[] = {&arg, &lay};
-  if (hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&prep_kernel<NP>),
-                                     dim3(uint32_t(lay.slots * p.Hv)), dim3(256), args, 0, st);
-      e != hipSuccess)
-    return e;
-  const int64_t pairs = int64_t(p.N) * p.Hv;
+  const int64_t wgs = seqs * p.Hv * (KIND == kSummary ? 2 : 1) * kD / (16 * W);
+  return hipLaunchKernel(reinterpret_cast<const void*>(&scan_kernel<NP, W, KIND>), dim3(uint32_t(wgs)),
+                         dim3(64 * W), args, 0, st);
+}
+
+template <int NP>
+hipError_t launch_prep(const GdrParams& p, GdrLayout lay, hipStream_t st) {
+  GdrParams arg = p;
+  void* args[] = {&arg, &lay};
+  return hipLaunchKernel(reinterpret_cast<const void*>(&prep_kernel<NP>), dim3(uint32_t(lay.slots * p.Hv)),
+                         dim3(256), args, 0, st);
+}
+
+template <int NP>
+hipError_t launch_whole(const GdrParams& p, const GdrLayout& lay, int cus, hipStream_t st) {
+  if (hipError_t e = launch_prep<NP>(p, lay, st); e != hipSuccess) return e;
   // A workgroup fills a compute unit's LDS, so with at most half as many states
   // as units two workgroups of 64 columns each take one: 8 x 2048 tokens, 16
   // heads 129 us against 155, 1 x 8192, 8 heads 280 against 366; above that one
   // of 128 columns and two waves per SIMD: 32 ragged prompts, 32 heads 326
   // against 417.
-  const bool two = 2 * pairs <= cus;
-  return hipLaunchKernel(two ? reinterpret_cast<const void*>(&scan_kernel<NP, 4>)
-                             : reinterpret_cast<const void*>(&scan_kernel<NP, 8>),
-                         dim3(uint32_t(pairs * (two ? 2 : 1))), dim3(two ? 256 : 512), args, 0, st);
+  return 2 * int64_t(p.N) * p.Hv <= cus ? launch_scan<NP, 4, kWhole>(p, lay, p.N, st)
+                                        : launch_scan<NP, 8, kWhole>(p, lay, p.N, st);
+}
+
+// The segment-parallel schedule, five launches.  Factors keep 22 bits whatever
+// the state's type: P and R are multiplied on.
+hipError_t launch_segments(const GdrParams& p, const GdrLayout& lay, int L, hipStream_t st) {
+  SegParams sp{};
+  sp.cu = p.cu;
+  sp.N = p.N;
+  sp.T = p.T;
+  sp.H = p.Hv;
+  sp.L = L;
+  sp.M = p.N + p.T / L;
+  sp.table = reinterpret_cast<int32_t*>(p.ws + lay.table);
+  sp.first = reinterpret_cast<int32_t*>(p.ws + lay.first);
+  sp.count = reinterpret_cast<int32_t*>(p.ws + lay.count);
+  sp.s0 = p.s0;
+  sp.s0_bf16 = p.state_bf16;
+  sp.summ = reinterpret_cast<const float*>(p.ws + lay.summ);
+  sp.starts = reinterpret_cast<float*>(p.ws + lay.starts);
+  GdrParams q = p;
+  q.seg = sp.table;
+  q.summ = reinterpret_cast<float*>(p.ws + lay.summ);
+  q.starts = sp.starts;
+  if (hipError_t e = launch_seg_plan(sp, st); e != hipSuccess) return e;
+  if (hipError_t e = launch_prep<2>(q, lay, st); e != hipSuccess) return e;
+  if (hipError_t e = launch_scan<2, 4, kSummary>(q, lay, sp.M, st); e != hipSuccess) return e;
+  if (hipError_t e = launch_seg_combine(sp, st); e != hipSuccess) return e;
+  return launch_scan<2, 4, kRerun>(q, lay, sp.M, st);
+}
+
+constexpr int kSegSlots = 160;      // (segment, head) pairs that the workspace holds
+constexpr int kSegMinTokens = 2048;  // of a call that takes segments
+
+// Tokens per segment, or 0 for whole sequences.  Measured, whole / segments
+// (us): 1 x 8192 tokens, 8 heads 305 / 157; 1 x 2048, 8 heads 110 / 74; 1 x
+// 16384, 16 heads 693 / 385; 2 x 4096, 16 heads 243 / 192 (207 with the shorter
+// segments that fewer states take); 1 x 4096, 32 heads 189 / 191; 1 x 2048, 16
+// heads 88 / 88; 1 x 1024, 2 heads 49 / 58.
+int segment_length(int64_t T, int Hv, int64_t N) {
+  const int64_t pairs = N * Hv;
+  if (pairs > 32 || T < (pairs > 8 ? 4096 : 2048) * N) return 0;
+  const int64_t target = std::max<int64_t>(1, (pairs > 16 ? 96 : 128) / Hv);
+  const int64_t L = std::max<int64_t>(256, ((T + target - 1) / target + kC - 1) / kC * kC);
+  return (N + T / L) * Hv <= kSegSlots ? int(L) : 0;
 }
 
 }  // namespace
@@ -643,12 +750,21 @@ GdrLayout gdr_layout(int64_t T, int Hk, int Hv, int64_t N) {
   l.head = 0;
   l.tri = l.head + up(size_t(l.slots) * Hk * kHeadUnits * 1024);
   l.coef = l.tri + up(size_t(l.slots) * Hv * kMaxTri * 1024);
-  l.total = l.coef + up(size_t(l.slots) * Hv * kCoefs * 4);
+  l.table = l.coef + up(size_t(l.slots) * Hv * kCoefs * 4);
+  // one size for every head count, so that the workspace's size grows with each argument
+  const size_t seg = T >= kSegMinTokens ? kSegSlots : 0, state = size_t(kD) * kD * 4;
+  l.first = l.table + up(16 * seg);
+  l.count = l.first + up(4 * seg);
+  l.summ = l.count + up(4 * seg);
+  l.starts = l.summ + 2 * seg * state;
+  l.total = l.starts + seg * state;
   return l;
 }
 
 hipError_t launch_gdr_chunked(const GdrParams& p, int cus, hipStream_t stream) {
-  return p.state_bf16 ? launch<1>(p, cus, stream) : launch<2>(p, cus, stream);
+  const GdrLayout lay = gdr_layout(p.T, p.Hk, p.Hv, p.N);
+  if (const int L = segment_length(p.T, p.Hv, p.N); L > 0) return launch_segments(p, lay, L, stream);
+  return p.state_bf16 ? launch_whole<1>(p, lay, cus, stream) : launch_whole<2>(p, lay, cus, stream);
 }
 
 }  // namespace kda

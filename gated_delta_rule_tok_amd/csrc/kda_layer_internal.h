@@ -29,6 +29,11 @@ struct GdrParams {
   int T, Hk, Hv, N;
   int state_bf16;
   char* ws;  // prefill: see gdr_layout
+  // segment-parallel schedule: its table (see SegParams), the summaries it
+  // writes, the states it starts from
+  const int32_t* seg;
+  float* summ;
+  const float* starts;
 };
 
 // Chunk slots: sequence n's j-th chunk has slot cu[n] / 64 + n + j.  The next
@@ -37,7 +42,8 @@ struct GdrParams {
 // cover every batch of N sequences and T tokens.
 struct GdrLayout {
   int64_t slots;
-  size_t head, tri, coef, total;  // byte offsets of the parts, and their sum
+  size_t head, tri, coef;             // byte offsets of the parts
+  size_t table, first, count, summ, starts, total;
 };
 GdrLayout gdr_layout(int64_t T, int Hk, int Hv, int64_t N);
 

@@ -177,6 +177,24 @@ def test_prefill(lens, hk, hv, state):
 
 
 @pytest.mark.parametrize("state", ["float32", "bfloat16"])
+@pytest.mark.parametrize("lens,hk,hv,init", [([2500], 1, 2, True), ([5000], 4, 8, False), ([2048], 1, 1, True),
+                                             ([9000, 0, 300, 1], 1, 2, True), ([4300, 4100], 8, 8, True)], ids=str)
+def test_prefill_in_segments(lens, hk, hv, init, state):
+    """Few states and long sequences: segments at once, joined by their maps;
+    one in five tokens almost erases the state, the others keep nearly all of
+    it.  Tokens behind the last sequence stay."""
+    import torch
+    dtype = getattr(torch, state)
+    x = Gdr(sum(lens) + 5, hk, hv, seed=len(lens) + hv, packed=True)
+    x.a = x.a - 6 + 14 * (torch.rand(x.a.shape, generator=_gen(1), device="cuda") < 0.2).bfloat16()
+    s0 = _state((len(lens), hv, D, D), dtype, 3) if init else None
+    out, fin = _prefill(x, lens, dtype, s0, fill=3.0)
+    assert (out[-5:] == 3.0).all()
+    _check_gdr(x, _spans(lens), out, fin, _reference(x, _spans(lens), s0), dtype, f"segments {lens} {state}",
+               rows=slice(0, sum(lens)), rms=True)
+
+
+@pytest.mark.parametrize("state", ["float32", "bfloat16"])
 @pytest.mark.parametrize("lens", [[1], [8], [3, 0, 8, 1, 20], [1] * 600], ids=lambda v: str(v)[:20])
 def test_prefill_of_few_tokens(lens, state):
     """At most 8 tokens per sequence: the serial kernel."""
