@@ -646,6 +646,8 @@ def kda_gdr_decode_step(q, k, v, a, beta_logits, A_log, dt_bias, scale: float, s
 
 def _row_stride(t, name):
     """Elements between the rows of a 2-D tensor whose rows are dense."""
+    if t.is_contiguous():
+        return t.shape[1]
     row, col = t.stride()
     if col != 1 and t.shape[1] > 1 and t.shape[0]:
         raise ValueError(f"{name} must have contiguous rows")

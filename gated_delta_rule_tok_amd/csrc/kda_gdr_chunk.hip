@@ -391,6 +391,7 @@ __device__ __forceinline__ float over_column(float m) {
 }
 
 enum { kWhole, kSummary, kRerun };
+constexpr uint32_t kRankGrid = 256;
 
 template <int NP, int W, int KIND>
 __global__ __launch_bounds__(64 * W, W / 4) void scan_kernel(GdrParams p, GdrLayout lay) {
@@ -408,6 +409,21 @@ __global__ __launch_bounds__(64 * W, W / 4) void scan_kernel(GdrParams p, GdrLay
   bool last = true;
   int64_t slot0;
   if (KIND == kWhole) {
+    // With more workgroups than fit at once the longest sequences go first
+    // (ties by index): 32 ragged prompts, 32 heads 291 us against 322.
+    if (p.N > 1 && p.N <= 64 && gridDim.x > kRankGrid) {
+      int len = -1;
+      if (lane < p.N) {
+        gdr_range(p, lane, t0, t1);
+        len = t1 - t0;
+      }
+      int rank = 0;
+      for (int j = 0; j < p.N; ++j) {
+        const int other = __builtin_amdgcn_readlane(len, j);
+        rank += other > len || (other == len && j < lane);
+      }
+      n = __builtin_ctzll(__ballot(lane < p.N && rank == m));
+    }
     gdr_range(p, n, t0, t1);
     slot0 = first_slot(p, n);
   } else {
@@ -692,7 +708,7 @@ hipError_t launch_whole(const GdrParams& p, const GdrLayout& lay, int cus, hipSt
   // as units two workgroups of 64 columns each take one: 8 x 2048 tokens, 16
   // heads 129 us against 155, 1 x 8192, 8 heads 280 against 366; above that one
   // of 128 columns and two waves per SIMD: 32 ragged prompts, 32 heads 326
-  // against 417.
+  // against 417 (sequences in index order).
   return 2 * int64_t(p.N) * p.Hv <= cus ? launch_scan<NP, 4, kWhole>(p, lay, p.N, st)
                                         : launch_scan<NP, 8, kWhole>(p, lay, p.N, st);
 }

@@ -100,9 +100,14 @@ size_t kda_gdr_get_workspace_size(int64_t max_tokens, int32_t key_heads, int32_t
  * a bf16 state (out, which is bf16, 11 bits either way), relative to the
  * largest element of their column: finite values and states of any size are
  * taken.  The final state and out are rounded once, at the end.
- * An input that is not finite makes the rows of its sequence and head from
- * its chunk of 64 tokens on, and their final state, undefined; other
- * sequences and heads are not affected.
+ * An input that is not finite makes the rows of its sequence and of the value
+ * heads that read it undefined from its chunk of 64 tokens on, and their
+ * final states; other sequences and heads are not affected.
+ *
+ * Calls with at most 8 tokens per sequence on average run token after token,
+ * others in chunks; up to 32 (sequence, value head) pairs with at least 2048
+ * tokens per sequence on average (4096 above 8 pairs) run in segments at once.
+ * These forms agree within the bounds above, not bit for bit.
  */
 kda_status_t kda_gdr_prefill_fwd(const void* q, const void* k, const void* v, const void* a,
                                  const void* beta_logits, const float* A_log, const float* dt_bias,
@@ -147,7 +152,9 @@ typedef enum { KDA_OUT_BF16 = 0, KDA_OUT_E4M3 = 1 } kda_out_dtype_t;
  *
  * with one scale per row (group_size 0) or per group_size = 128 channels (the
  * last group of a row may be shorter).  A group that is zero throughout gets
- * scale 0 and zeros.  y is formed from the unrounded s.
+ * scale 0 and zeros.  y is formed from the unrounded s.  Sums are fp32: a row
+ * whose sum of squares passes 3e38 gives zeros, one with an infinity or a NaN
+ * gives NaN (NaN scales).
  *
  *   x, residual  bf16 [num_rows, dim], rows x_row and residual_row elements
  *                apart, dim contiguous
@@ -181,7 +188,11 @@ kda_status_t kda_add_rms_norm(const void* x, void* residual, const void* weight,
  *
  * group_size is 32, 64 or 128, k a positive multiple of it (at most 2^20),
  * 1 <= n <= 2^24, 0 <= num_tokens <= 64; x and w are 16-byte aligned.  Sums
- * are fp32.  No workspace.  x may be NULL when num_tokens is 0.
+ * are fp32 of exact products.  A value of x that is not finite makes its row of
+ * y NaN, other rows are not affected; a row's result does not depend on the
+ * rows beside it within the same kernel (1..4, 5..16, 17..32 and 33..64 tokens
+ * may differ in the order of the sums).  No workspace.  x may be NULL when
+ * num_tokens is 0.
  */
 kda_status_t kda_w4_proj(const void* x, const void* w, const void* scales, const void* zeros,
                          void* y, void* stream, int32_t num_tokens, int32_t k, int32_t n,
