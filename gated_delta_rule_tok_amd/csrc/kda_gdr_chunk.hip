@@ -90,12 +90,10 @@ constexpr int kPitch = 68;  // floats per row of the LDS matrices (bank spread)
 struct PrepLds {
   union {
     bf16x8 kf[4][4][64];    // K as operand units [tile][k-step][lane], until A and P are formed
-    struct {
-      _Float16 P[kC][72];
-      float tmp[4][16][17];
-    };
+    float A[kC][kPitch];    // A below the diagonal; T in the diagonal blocks; T_ij in block (j, i)
   };
-  float A[kC][kPitch];      // A below the diagonal; T in the diagonal blocks; T_ij in block (j, i)
+  _Float16 P[kC][72];
+  float tmp[4][16][16];
   double G[kC];
   float rk[kC], rq[kC], beta[kC], kd[kC], qd[kC];
 };
@@ -114,22 +112,19 @@ __device__ __forceinline__ f32x4 block_mul(const float* X, int xp, const float* 
   return acc;
 }
 
-// One row of K or Q: this lane's 32 channels (32 s + 8 g4 ..), the factor that
-// makes it a unit row, and the power of two that brings its largest element to
-// [1, 2).
-__device__ __forceinline__ void load_row(const uint16_t* row, bool ok, bf16x8 (&out)[4], float& unit, float& down) {
+// One row of K or Q, this lane's 32 channels of it: the factor that makes it a
+// unit row, and the power of two that brings its largest element to [1, 2).
+__device__ __forceinline__ void row_factors(const bf16x8 (&row)[4], float& unit, float& down) {
   float sum = 0.f, big = 0.f;
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    const uint4 raw = *reinterpret_cast<const uint4*>(row + 32 * s);
     float f[8];
-    unpack8(raw, f);
+    unpack8(__builtin_bit_cast(uint4, row[s]), f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       sum = fmaf(f[j], f[j], sum);
       big = fmaxf(big, fabsf(f[j]));
     }
-    out[s] = __builtin_bit_cast(bf16x8, raw);
   }
   sum += __shfl_xor(sum, 16);
   big = fmaxf(big, __shfl_xor(big, 16));
@@ -137,7 +132,7 @@ __device__ __forceinline__ void load_row(const uint16_t* row, bool ok, bf16x8 (&
   big = fmaxf(big, __shfl_xor(big, 32));
   const uint32_t e = __float_as_uint(big) >> 23;  // 0: nothing but zeros (or less than fp32 squares hold)
   down = e ? __uint_as_float((254u - min(e, 253u)) << 23) : 1.f;
-  unit = ok ? 1.f / sqrtf(sum + kNormEps) : 0.f;
+  unit = 1.f / sqrtf(sum + kNormEps);
 }
 
 // Eight bf16 times a power of two, in fp16
@@ -156,35 +151,65 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(GdrParams p, GdrLayout lay
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t slot = blockIdx.x / p.Hv;
-  const int h = blockIdx.x % p.Hv, hk = h / (p.Hv / p.Hk);
-  // the last sequence whose first slot is not behind this one, 64 candidates at a time
-  int lo = 0;
-  for (int span = p.N; span > 1;) {
-    const int step = (span + 63) / 64, n = lo + lane * step;
-    const bool in = lane * step < span && first_slot(p, min(n, p.N - 1)) <= slot;
-    const int k = 63 - __builtin_clzll(__ballot(in) | 1);
-    lo += k * step;
-    span = min(step, span - k * step);
+  const int h = blockIdx.x % p.Hv, group = p.Hv / p.Hk, hk = h / group;
+  // the last sequence whose first slot is not behind this one, 64 candidates at
+  // a time; its range comes from the same loads where 64 hold them all
+  int lo = 0, t0, t1;
+  if (p.N <= 64) {
+    gdr_range(p, min(lane, p.N - 1), t0, t1);
+    lo = 63 - __builtin_clzll(__ballot(lane < p.N && t0 / kC + lane <= slot) | 1);
+    t0 = __builtin_amdgcn_readlane(t0, lo);
+    t1 = __builtin_amdgcn_readlane(t1, lo);
+  } else {
+    for (int span = p.N; span > 1;) {
+      const int step = (span + 63) / 64, n = lo + lane * step;
+      const bool in = lane * step < span && first_slot(p, min(n, p.N - 1)) <= slot;
+      const int k = 63 - __builtin_clzll(__ballot(in) | 1);
+      lo += k * step;
+      span = min(step, span - k * step);
+    }
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    gdr_range(p, lo, t0, t1);
   }
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  int t0, t1;
-  gdr_range(p, lo, t0, t1);
-  const int64_t off = (slot - first_slot(p, lo)) * kC;
+  const int64_t off = (slot - (t0 / kC + lo)) * kC;
   if (off < 0 || off >= t1 - t0) return;  // no chunk has this slot
   t0 += int(off);
   const int len = min(kC, t1 - t0);
-  const bool first = h % (p.Hv / p.Hk) == 0;  // writes K, Q and K^T for the key head's value heads
+  const bool first = h % group == 0;  // writes K, Q and K^T for the key head's value heads
   f16x8* units = reinterpret_cast<f16x8*>(p.ws + lay.head) + (size_t(slot) * p.Hk + hk) * (kHeadUnits * 64) + lane;
 
   // rows of K and Q as operands: lane l row l % 16 of tile w, channels 32 s + 8
   // (l / 16); rows behind the end repeat the last one, with factors of 0
+  // (every load of the workgroup's inputs is issued before the first is used)
   bf16x8 kf[4], qf[4];
+  const int r0 = 16 * w + l16;
   {
-    const int r = 16 * w + l16;
-    const int64_t t = t0 + min(r, len - 1);
+    const int64_t t = t0 + min(r0, len - 1);
+    const uint16_t* kp = p.k + t * p.k_t + hk * p.k_h + 8 * g4;
+    const uint16_t* qp = p.q + t * p.q_t + hk * p.q_h + 8 * g4;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) kf[s] = *reinterpret_cast<const bf16x8*>(kp + 32 * s);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) qf[s] = *reinterpret_cast<const bf16x8*>(qp + 32 * s);
+  }
+  const int64_t tg = t0 + min(lane, len - 1);  // gates: lane = token
+  const uint16_t raw_a = p.a[tg * p.a_t + h * p.a_h], raw_beta = p.beta[tg * p.b_t + h * p.b_h];
+  const float A_log = p.A_log[h], dt_bias = p.dt_bias[h];
+  // G in fp64, so that differences of large sums keep their small terms, and times log2(e)
+  if (w == 0) {
+    double G = lane < len ? double(gdr_log_decay(bf16_to_f32(raw_a), A_log, dt_bias)) * 1.4426950408889634074 : 0.0;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const double u = __shfl_up(G, o);
+      if (lane >= o) G += u;
+    }
+    L.G[lane] = G;
+    L.beta[lane] = lane < len ? gdr_sigmoid(bf16_to_f32(raw_beta)) : 0.f;
+  }
+  {
     float rk, rq, kd, qd;
-    load_row(p.k + t * p.k_t + hk * p.k_h + 8 * g4, r < len, kf, rk, kd);
-    load_row(p.q + t * p.q_t + hk * p.q_h + 8 * g4, r < len, qf, rq, qd);
+    row_factors(kf, rk, kd);
+    row_factors(qf, rq, qd);
 #pragma unroll
     for (int s = 0; s < 4; ++s) L.kf[w][s][lane] = kf[s];
     if (first) {
@@ -195,26 +220,11 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(GdrParams p, GdrLayout lay
       }
     }
     if (g4 == 0) {
-      L.rk[r] = rk;
-      L.rq[r] = rq;
-      L.kd[r] = kd;
-      L.qd[r] = qd;
+      L.rk[r0] = r0 < len ? rk : 0.f;
+      L.rq[r0] = r0 < len ? rq : 0.f;
+      L.kd[r0] = kd;
+      L.qd[r0] = qd;
     }
-  }
-  // gates: lane = token; G in fp64, so that differences of large sums keep their
-  // small terms, and times log2(e)
-  if (w == 0) {
-    const bool ok = lane < len;
-    const int64_t t = t0 + (ok ? lane : 0);
-    const float la = gdr_log_decay(bf16_to_f32(p.a[t * p.a_t + h * p.a_h]), p.A_log[h], p.dt_bias[h]);
-    double G = ok ? double(la) * 1.4426950408889634074 : 0.0;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const double u = __shfl_up(G, o);
-      if (lane >= o) G += u;
-    }
-    L.G[lane] = G;
-    L.beta[lane] = ok ? gdr_sigmoid(bf16_to_f32(p.beta[t * p.b_t + h * p.b_h])) : 0.f;
   }
   __syncthreads();
   // K transposed, as operand units [state tile r][k-step z]: lane l the channel
@@ -248,21 +258,37 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(GdrParams p, GdrLayout lay
     co[kUs * kC] = rk * ex2(float(Gend - L.G[tid]));
     co[kEnd * kC] = ex2(float(Gend));
   }
-  // A and P, row tile w
+  // A and P, row tile w (Q first, so that its rows' registers are free for K's products)
   f32x4 kk[4], qk[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    kk[j] = qk[j] = f32x4{};
+    qk[j] = f32x4{};
     if (j <= w) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const bf16x8 b = L.kf[j][s][lane];
-        kk[j] = mfma32(kf[s], b, kk[j]);
-        qk[j] = mfma32(qf[s], b, qk[j]);
-      }
+      for (int s = 0; s < 4; ++s) qk[j] = mfma32(qf[s], L.kf[j][s][lane], qk[j]);
     }
   }
-  __syncthreads();  // kf is read: P takes its place
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    kk[j] = f32x4{};
+    if (j <= w) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) kk[j] = mfma32(kf[s], L.kf[j][s][lane], kk[j]);
+    }
+  }
+  __syncthreads();  // kf is read: A takes its place
+  // (the rows' factors first, and selects after the products: conditions around
+  // LDS reads become branches, and the reads wait for each other)
+  double Gt[4];
+  float bt[4], qt[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = 16 * w + 4 * g4 + i;
+    Gt[i] = L.G[t];
+    bt[i] = L.beta[t] * L.rk[t];
+    qt[i] = L.rq[t];
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int s = 16 * j + l16;
@@ -278,18 +304,21 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(GdrParams p, GdrLayout lay
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = 16 * w + 4 * g4 + i;
-      const float e = ex2(float(L.G[t] - Gs)) * rs;
-      L.A[t][s] = s < t ? L.beta[t] * L.rk[t] * e * kk[j][i] : 0.f;
-      L.P[t][s] = (_Float16)(s <= t ? L.rq[t] * e * qk[j][i] : 0.f);
+      const float e = ex2(float(Gt[i] - Gs)) * rs, a = bt[i] * e * kk[j][i], q = qt[i] * e * qk[j][i];
+      L.A[t][s] = s < t ? a : 0.f;
+      L.P[t][s] = (_Float16)(s <= t ? q : 0.f);
     }
   }
   // T: the diagonal blocks by forward substitution, a column per lane
   {
     wave_sync();
+    __builtin_amdgcn_sched_barrier(0);
     float x[16];
     const float* a = &L.A[16 * w][16 * w];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
+      // (a few rows' elements of A at a time: all 120 would not leave the registers for five workgroups)
+      if (i % 6 == 5) __builtin_amdgcn_sched_barrier(0);
       float v = i == l16 ? 1.f : 0.f;
 #pragma unroll
       for (int j = 0; j < i; ++j) v = fmaf(-a[i * kPitch + j], x[j], v);
@@ -314,7 +343,7 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(GdrParams p, GdrLayout lay
 #pragma unroll
       for (int i = 0; i < 4; ++i) L.tmp[w][4 * g4 + i][l16] = acc[i];
       wave_sync();
-      const f32x4 t = block_mul(&L.A[16 * w][16 * w], kPitch, &L.tmp[w][0][0], 17, f32x4{}, l16, g4);
+      const f32x4 t = block_mul(&L.A[16 * w][16 * w], kPitch, &L.tmp[w][0][0], 16, f32x4{}, l16, g4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) L.A[16 * j + 4 * g4 + i][16 * w + l16] = -t[i];
     }
