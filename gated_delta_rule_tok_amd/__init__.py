@@ -12,6 +12,12 @@ is no CPU fallback: if libkda.so is missing, every call raises.
 q, k, v, g, out and beta_logits may be strided views (channels contiguous, for
 [T, H, 128] both strides multiples of 8 elements): they then go through
 kda_chunk_prefill_fwd_strided, with no copy.
+
+The operators around the forward (include/kda_layer.h) are here too:
+
+    kda_add_rms_norm(x, residual, weight, 1e-6, hidden)
+    kda_w4_proj(hidden, w, scales, None, qkvab, 128)
+    kda_gdr_decode_step(q, k, v, a, beta_logits, A_log, dt_bias, scale, pool, slots, out)
 """
 from __future__ import annotations
 

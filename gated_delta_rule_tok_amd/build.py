@@ -51,7 +51,8 @@ def hipcc() -> str:
 
 
 def sources() -> list[str]:
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".hip"))
+    return sorted(os.path.join(d, f) for d in (CSRC, os.path.join(CSRC, "layer"))
+                  for f in os.listdir(d) if f.endswith(".hip"))
 
 
 def _compile(src: str) -> str:

@@ -18,7 +18,6 @@
 
 #include "kda.h"
 #include "kda_internal.h"
-#include "kda_layer_internal.h"
 
 namespace {
 
@@ -517,6 +516,7 @@ kda_status_t forward(const void* q, const void* k, const void* v, const void* g,
 
 }  // namespace
 
+// For the layer operators' host code (csrc/layer): the same error text, the same device query.
 namespace kda {
 int record_hip_failure(hipError_t e, const char* step) { return hip_failure(e, step); }
 hipError_t device_cus(int* cus) { return device_cu_count(cus); }

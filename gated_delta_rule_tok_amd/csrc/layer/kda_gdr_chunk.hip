@@ -11,8 +11,15 @@
 //
 // Two launches.  prep_kernel, one workgroup per (chunk, value head), forms
 // what does not depend on the state, for all chunks at once: T, the matrix P
-// in front of U, the coefficients of every token, and K and Q as operands.
+// in front of U, the coefficients of every token, and K, Q and K^T as operands.
 // scan_kernel walks the chunks of a sequence with the state in registers.
+//
+// What bounds it.  A chunk depends on the one before, about 750 instructions of
+// a wave, 2.2 us; 8 x 2048 tokens, 16 heads, fp32 state: prep 62 us, scan 128
+// us (219 MB of inputs and outputs: 43 us at the rate of a copy).  With more
+// states than compute units it is the bytes too: 32 ragged prompts, 32 heads,
+// bf16 state, prep 215 us and scan 291 us for 1.7 GB, the operands that prep
+// writes and scan reads among them.
 //
 // Precision.  Operands are fp16 (11 bits), sums fp32.
 //  * A row of K or Q, times a power of two that brings its largest element to
@@ -27,7 +34,7 @@
 //    so each column carries a power of two per chunk that brings the larger of
 //    its |S| and |v| to [2^7, 2^8).  ||S_t|| grows by at most |v| per token
 //    (the map is a contraction), hence |U| <= (1 + sqrt(128) + 64) 2^8 < 2^15:
-//    no finite input overflows, and what fp16 loses below 2^-14 is under 2^-32
+//    no finite input overflows, and what fp16 loses below 2^-14 is under 2^-28
 //    of the column's largest element.  T and P are at most 1.
 #include <algorithm>
 #include <type_traits>
