@@ -324,7 +324,7 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(GdrParams p, GdrLayout lay
     const float* a = &L.A[16 * w][16 * w];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      // (a few rows' elements of A at a time: all 120 would not leave the registers for five workgroups)
+      // (a few rows' elements of A at a time: all 120 in flight spill)
       if (i % 6 == 5) __builtin_amdgcn_sched_barrier(0);
       float v = i == l16 ? 1.f : 0.f;
 #pragma unroll

@@ -47,7 +47,7 @@ struct GdrLayout {
 };
 GdrLayout gdr_layout(int64_t T, int Hk, int Hv, int64_t N);
 
-// Chunked prefill: two launches.
+// Chunked prefill: two launches, five where sequences are cut into segments.
 hipError_t launch_gdr_chunked(const GdrParams& p, int cus, hipStream_t stream);
 // Token after token, for the single-token step and sequences of few tokens.
 hipError_t launch_gdr_serial(const GdrParams& p, hipStream_t stream);

@@ -159,11 +159,13 @@ def _check_gdr(x, spans, out, fin, ref, dtype, label, rows=None, rms=False):
 CHUNKED = [
     ([100], 1, 1), ([64], 2, 4), ([65, 1, 0, 63, 130], 2, 2), ([200, 129], 1, 4), ([16, 17, 33, 48, 49], 3, 9),
     ([700], 5, 5), ([1, 300, 1, 0, 0, 128], 2, 6), ([9] * 20, 1, 2), ([257] * 40, 1, 2),
+    # more sequences than a wave holds; more workgroups than run at once, longest sequences first
+    ([10] * 100 + [70, 0, 200, 64, 1], 1, 2), ([i * 37 % 150 for i in range(33)], 4, 8),
 ]
 
 
 @pytest.mark.parametrize("state", ["float32", "bfloat16"])
-@pytest.mark.parametrize("lens,hk,hv", CHUNKED, ids=str)
+@pytest.mark.parametrize("lens,hk,hv", CHUNKED, ids=lambda v: str(v)[:24])
 def test_prefill(lens, hk, hv, state):
     """Both forms of the scan (few and many workgroups), ragged and empty
     sequences, shared key heads, with an initial state."""
