@@ -63,8 +63,8 @@ struct Block {
   u32x4 w[NT], x[MT][RQ];
 };
 
-// MT tiles of 16 tokens (the first 4 RQ rows of each hold tokens), NT tiles of
-// 16 rows of w per workgroup, WAVES waves that share k, U blocks in flight per
+// MT tiles of 16 tokens (the first 4 RQ rows of each hold tokens) and NT tiles
+// of 16 rows of w per workgroup, WAVES waves that share k, U blocks in flight per
 // wave; G the group.
 template <int MT, int RQ, int NT, int WAVES, int U, int G, bool ZERO>
 __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Params p) {
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Params p) {
   uint32_t* sz = reinterpret_cast<uint32_t*>(lds + kXBytes);  // [16 NT][kScalePitch]: scale | zero << 16
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
-  const int n0 = blockIdx.x * (16 * NT);
+  const int n0 = blockIdx.x * (16 * NT), m0 = blockIdx.y * (16 * MT);
   const int groups = p.K / G, blocks = (p.K + 127) / 128;
   // rows behind the last row or token repeat it: their sums are not stored
   // (32-bit offsets from scalar bases: 64 rows of at most 2^19 bytes of w, and of 2^20 elements of x)
@@ -91,7 +91,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Params p) {
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < RQ; ++j) xrow[i][j] = uint32_t(min(16 * i + 4 * j + g4, p.M - 1) * p.x_row);
+    for (int j = 0; j < RQ; ++j) xrow[i][j] = uint32_t(min(m0 + 16 * i + 4 * j + g4, p.M - 1) * p.x_row);
   const uint32_t xpiece = 8 * l16, xtail = min(8 * l16, max(p.K - 8 - last, 0));
   // this wave's x, 256 bytes a row, its 16-byte pieces in the order piece ^ row (bank spread)
   char* xl = lds + wave * (MT * 4096);
@@ -217,7 +217,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Params p) {
     const int n = n0 + 16 * (i % NT) + l16;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int m = 16 * (i / NT) + 4 * g4 + r;
+      const int m = m0 + 16 * (i / NT) + 4 * g4 + r;
       if (m < p.M && n < p.N) p.y[size_t(m) * p.y_row + n] = f32_to_bf16(y[r]);
     }
   }
@@ -237,7 +237,8 @@ hipError_t launch(const W4Params& p, hipStream_t st) {
   const void* f = p.group == 32   ? kernel<MT, RQ, NT, WAVES, U, 32>(z)
                   : p.group == 64 ? kernel<MT, RQ, NT, WAVES, U, 64>(z)
                                   : kernel<MT, RQ, NT, WAVES, U, 128>(z);
-  return hipLaunchKernel(f, dim3((p.N + 16 * NT - 1) / (16 * NT)), dim3(64 * WAVES), args, 0, st);
+  const dim3 grid((p.N + 16 * NT - 1) / (16 * NT), (p.M + 16 * MT - 1) / (16 * MT));
+  return hipLaunchKernel(f, grid, dim3(64 * WAVES), args, 0, st);
 }
 
 }  // namespace
@@ -245,18 +246,23 @@ hipError_t launch(const W4Params& p, hipStream_t st) {
 // Rows of w per workgroup: 32 read x half as often as 16, 16 give twice the
 // workgroups.  Measured (us, 16 / 32 rows): 16 tokens x 7168 x 1536 7.3 / 9.0,
 // x 2048 x 4096 4.8 / 5.5, x 4096 x 5120 8.6 / 8.0, x 7168 x 14336 26.9 / 20.4;
-// 64 x 7168 x 1536 20.0 / 23.8, 61 x 2048 x 7171 18.8 / 12.6; with at most 4
-// tokens x is a quarter of that: 4 x 7168 x 7168 11.3 / 11.5, 2 x 7168 x 14336
-// 17.2 / 15.8.  So 32 from half a workgroup of them per compute unit on, and
-// from one and a half on with at most 4 tokens.  64 rows lose everywhere.
+// 24 x 7168 x 1536 7.6 / 9.5, 32 x 512 x 3000 6.2 / 4.4, 64 x 7168 x 1536 14.2 /
+// 10.5, 64 x 2048 x 512 4.5 / 5.6: 32 where they are more than half a workgroup
+// per compute unit.  With at most 4 tokens x is a quarter of that: 4 x 7168 x
+// 7168 11.3 / 11.5, 2 x 7168 x 14336 17.2 / 15.8, so 32 from one and a half on.
+// 64 rows lose everywhere.
+//
+// Tokens per workgroup: more than 16 in tiles of 16, each with workgroups of its
+// own that read w again (64 x 7168 x 1536 10.5 us against 20.4 with all 64 in
+// one, 24 x 7168 x 7168 17.0 against 18.5 with 32), but more than 32 with many
+// rows of w in one (61 x 2048 x 7171 12.4 against 17.8, 64 x 7168 x 7168 30.6
+// against 33.0).
 hipError_t launch_w4(const W4Params& p, int cus, hipStream_t stream) {
-  const int wide = (p.N + 31) / 32;
+  const int64_t wide = (p.N + 31) / 32, tiles = (p.M + 15) / 16;
   if (p.M <= 4)
     return 2 * wide > 3 * cus ? launch<1, 1, 2, 8, 2>(p, stream) : launch<1, 1, 1, 8, 2>(p, stream);
-  const bool two = 2 * wide > cus;
-  if (p.M <= 16) return two ? launch<1, 4, 2, 8, 1>(p, stream) : launch<1, 4, 1, 16, 1>(p, stream);
-  if (p.M <= 32) return two ? launch<2, 4, 2, 8, 1>(p, stream) : launch<2, 4, 1, 8, 2>(p, stream);
-  return two ? launch<4, 4, 2, 8, 1>(p, stream) : launch<4, 4, 1, 8, 1>(p, stream);
+  if (p.M > 32 && 2 * wide > cus) return launch<4, 4, 2, 8, 1>(p, stream);
+  return 2 * wide * tiles > cus ? launch<1, 4, 2, 8, 1>(p, stream) : launch<1, 4, 1, 16, 1>(p, stream);
 }
 
 }  // namespace kda
