@@ -545,6 +545,8 @@ def _w4_check(x, w, s, z, group, y, label):
     (17, 1024, 16, 128), (31, 1152, 15, 128), (33, 4128, 70, 32), (64, 2048, 145, 64), (5, 1088, 144, 64),
     (1, 128, 5000, 128), (64, 16384, 3, 128), (50, 512, 4200, 64), (33, 256, 4111, 128), (20, 256, 5000, 32),
     (3, 256, 12400, 64), (16, 384, 4300, 128),
+    # more groups than LDS holds scales of at a time
+    (5, 9632, 40, 32), (16, 17408, 33, 64), (40, 4192, 4100, 32), (1, 33024, 17, 128),
 ])
 def test_w4(m, k, n, group, zeros):
     import torch
