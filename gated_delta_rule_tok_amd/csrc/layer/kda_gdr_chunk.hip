@@ -14,11 +14,11 @@
 // in front of U, the coefficients of every token, and K, Q and K^T as operands.
 // scan_kernel walks the chunks of a sequence with the state in registers.
 //
-// What bounds it.  A chunk depends on the one before, about 750 instructions of
-// a wave, 2.2 us; 8 x 2048 tokens, 16 heads, fp32 state: prep 62 us, scan 128
-// us (219 MB of inputs and outputs: 43 us at the rate of a copy).  With more
+// What bounds it.  A chunk depends on the one before, 4 us with an fp32 state;
+// 8 x 2048 tokens, 16 heads, fp32 state: prep 68 us, scan 136 us (medians of a
+// trace; 219 MB of inputs and outputs: 43 us at the rate of a copy).  With more
 // states than compute units it is the bytes too: 32 ragged prompts, 32 heads,
-// bf16 state, prep 215 us and scan 291 us for 1.7 GB, the operands that prep
+// bf16 state, prep 222 us and scan 283 us for 1.7 GB, the operands that prep
 // writes and scan reads among them.
 //
 // Precision.  Operands are fp16 (11 bits), sums fp32.

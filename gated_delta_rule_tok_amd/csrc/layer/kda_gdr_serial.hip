@@ -9,7 +9,7 @@
 // (o from the old state, so that k and q share one reduction and one barrier).
 // A decode step is bound by the state's bytes, read and written once: every
 // load of the state is issued before anything else, 16 bytes per lane, 32 KB in
-// flight per workgroup.  256 sequences x 16 heads, fp32: 108.6 us, 5.0 TB/s (a
+// flight per workgroup.  256 sequences x 16 heads, fp32: 110 us, 4.9 TB/s (a
 // copy reaches 5.1).
 #include "kda_gdr.h"
 

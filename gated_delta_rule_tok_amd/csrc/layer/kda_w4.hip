@@ -22,8 +22,8 @@
 // sums through LDS in wave order.  What costs most beside the weights is x,
 // which every workgroup reads whole, and the scales; both go through LDS so
 // that their loads take whole cache lines.  16 tokens x 7168 x 14336 in groups
-// of 64 with zeros: 20.4 us (58 MB, 2.8 TB/s; a copy reaches 5.1); without the
-// loads of x and of the scales it took 14.
+// of 64 with zeros: 18.4 us (58 MB, 3.2 TB/s; a copy reaches 5.1); an earlier
+// form that took 20.4 us took 14 without the loads of x and of the scales.
 #include "kda_layer_internal.h"
 #include "kda_mfma.h"
 
