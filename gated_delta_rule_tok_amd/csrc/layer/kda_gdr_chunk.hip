@@ -120,7 +120,10 @@ __device__ __forceinline__ f32x4 block_mul(const float* X, int xp, const float* 
 }
 
 // One row of K or Q, this lane's 32 channels of it: the factor that makes it a
-// unit row, and the power of two that brings its largest element to [1, 2).
+// unit row, and the power of two that brings its largest element to [1, 2) (2^127
+// where that is no normal number, a row of zeros among them: the scaled row's
+// factor unit / down is then at most 1 like any other's, where 1 / 1e-3 of an
+// unscaled row of zeros would take W = unit U past fp16).
 __device__ __forceinline__ void row_factors(const bf16x8 (&row)[4], float& unit, float& down) {
   float sum = 0.f, big = 0.f;
 #pragma unroll
@@ -137,8 +140,8 @@ __device__ __forceinline__ void row_factors(const bf16x8 (&row)[4], float& unit,
   big = fmaxf(big, __shfl_xor(big, 16));
   sum += __shfl_xor(sum, 32);
   big = fmaxf(big, __shfl_xor(big, 32));
-  const uint32_t e = __float_as_uint(big) >> 23;  // 0: nothing but zeros (or less than fp32 squares hold)
-  down = e ? __uint_as_float((254u - min(e, 253u)) << 23) : 1.f;
+  const uint32_t e = __float_as_uint(big) >> 23;
+  down = __uint_as_float((254u - min(e, 253u)) << 23);
   unit = 1.f / sqrtf(sum + kNormEps);
 }
 

@@ -311,6 +311,22 @@ def test_zero_rows():
     _check_gdr(x, [(0, 90)], out, fin, _reference(x, [(0, 90)], None), torch.float32, "zero rows")
 
 
+@pytest.mark.parametrize("state", ["float32", "bfloat16"])
+@pytest.mark.parametrize("lens", [[150], [6], [2300]], ids=str)
+def test_zero_keys_that_nothing_forgets(lens, state):
+    """Keys of zeros, and of less than a normal number, with values beside them
+    and hardly any decay up to the chunk's end: no update, no overflow."""
+    import torch
+    dtype = getattr(torch, state)
+    x = Gdr(lens[0], 1, 2, seed=18)
+    x.dt_bias = x.dt_bias - 9
+    x.k[lens[0] // 3:lens[0] // 2] = 0
+    x.k[lens[0] - 3] = 1e-39
+    s0 = _state((1, 2, D, D), dtype, 9)
+    out, fin = _prefill(x, lens, dtype, s0)
+    _check_gdr(x, _spans(lens), out, fin, _reference(x, _spans(lens), s0), dtype, f"zero keys {lens} {state}")
+
+
 @pytest.mark.parametrize("lens", [[130, 100, 70], [2, 3, 4]], ids=str)
 def test_what_is_not_finite_stays_in_its_sequence_and_head(lens):
     import torch
