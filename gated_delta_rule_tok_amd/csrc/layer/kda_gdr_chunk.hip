@@ -585,11 +585,12 @@ __global__ __launch_bounds__(64 * W, W / 4) void scan_kernel(GdrParams p, GdrLay
       const float big = over_column(fmaxf(ms * inv, mv));
       const uint32_t e = __float_as_uint(big) >> 23, now = max(e, 27u) - 7u, old = __float_as_uint(inv) >> 23;
       if (__any(now > old || now + 4 < old)) {
+        // (to the true size and from there: sc * inv alone passes fp32 where a
+        // large column was erased and zeros follow)
         sc = __uint_as_float((254u - now) << 23);
-        const float ratio = sc * inv;
-        inv = __uint_as_float(now << 23);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) S[r] *= ratio;
+        for (int r = 0; r < 8; ++r) S[r] = S[r] * inv * sc;
+        inv = __uint_as_float(now << 23);
       }
     }
     // K S and Q S

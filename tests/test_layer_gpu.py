@@ -290,6 +290,36 @@ def test_values_and_states_of_any_size(size, state):
         assert d.norm() <= (2.3e-6 if dtype == torch.float32 else 2.4e-3) * y.norm()
 
 
+@pytest.mark.parametrize("state", ["float32", "bfloat16"])
+@pytest.mark.parametrize("lens", [[500], [2500], [8]], ids=str)
+@pytest.mark.parametrize("size", [1e9, 1e30, 1e37])
+def test_large_states_that_are_forgotten(lens, state, size):
+    """A column far above one is erased, then values of zero in whole chunks:
+    zeros, not 0 times infinity; values that follow are those of a new sequence."""
+    import torch
+    dtype = getattr(torch, state)
+    n = lens[0]
+    x = Gdr(n, 1, 2, seed=19)
+    x.a[:] = 100.0
+    keep = x.v.clone()
+    x.v[:] = 0
+    s0 = _state((1, 2, D, D), dtype, 10).clamp(-1, 1)
+    s0[:, 0, :, ::2] *= size
+    out, fin = _prefill(x, lens, dtype, s0)
+    assert (out == 0).all() and (fin == 0).all()
+    if n > 192:
+        x.a[192:] = -1.0
+        x.v[192:, :, 1:] = keep[192:, :, 1:]  # column 0 stays zero
+        x.v[192:] *= 1e-9
+        out, fin = _prefill(x, lens, dtype, s0)
+        assert (out[:192] == 0).all() and (out[..., 0] == 0).all() and (fin[..., 0] == 0).all()
+        y = Gdr(n - 192, 1, 2, seed=19)
+        for f in ("q", "k", "v", "a", "beta"):
+            setattr(y, f, getattr(x, f)[192:])
+        y.A_log, y.dt_bias = x.A_log, x.dt_bias
+        _check_gdr(y, [(0, y.T)], out[192:], fin, _reference(y, [(0, y.T)], None), dtype, f"forgotten {size} {state}")
+
+
 @pytest.mark.parametrize("size", [1e-18, 1e15])
 def test_keys_and_queries_of_any_size(size):
     import torch
