@@ -96,13 +96,13 @@ constexpr int kPitch = 68;  // floats per row of the LDS matrices (bank spread)
 
 struct PrepLds {
   union {
-    bf16x8 kf[4][4][64];    // K as operand units [tile][k-step][lane], until A and P are formed
+    f16x8 kf[4][4][64];     // K as operand units [tile][k-step][lane], until A and P are formed
     float A[kC][kPitch];    // A below the diagonal; T in the diagonal blocks; T_ij in block (j, i)
   };
   _Float16 P[kC][72];
   float tmp[4][16][16];
   double G[kC];
-  float rk[kC], rq[kC], beta[kC], kd[kC], qd[kC];
+  float rk[kC], rq[kC], beta[kC];
 };
 
 __device__ __forceinline__ void wave_sync() {
@@ -119,40 +119,44 @@ __device__ __forceinline__ f32x4 block_mul(const float* X, int xp, const float* 
   return acc;
 }
 
-// One row of K or Q, this lane's 32 channels of it: the factor that makes it a
-// unit row, and the power of two that brings its largest element to [1, 2) (2^127
-// where that is no normal number, a row of zeros among them: the scaled row's
-// factor unit / down is then at most 1 like any other's, where 1 / 1e-3 of an
-// unscaled row of zeros would take W = unit U past fp16).
-__device__ __forceinline__ void row_factors(const bf16x8 (&row)[4], float& unit, float& down) {
-  float sum = 0.f, big = 0.f;
+// One row of K or Q, this lane's 32 channels of it, times the power of two that
+// brings its largest element to [1, 2) (2^127 where that is no normal number, a
+// row of zeros among them), in fp16, and the factor that makes this scaled row a
+// unit one.  The sum of squares is the scaled row's: that of a row as it came
+// may pass fp32, as may its products with other rows.  The factor is at most 1:
+// W = factor U stays in fp16.
+__device__ __forceinline__ void scale_row(const bf16x8 (&row)[4], f16x8 (&half)[4], float& unit) {
+  float big = 0.f;
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     float f[8];
     unpack8(__builtin_bit_cast(uint4, row[s]), f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      sum = fmaf(f[j], f[j], sum);
-      big = fmaxf(big, fabsf(f[j]));
-    }
+    for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(f[j]));
   }
-  sum += __shfl_xor(sum, 16);
   big = fmaxf(big, __shfl_xor(big, 16));
-  sum += __shfl_xor(sum, 32);
   big = fmaxf(big, __shfl_xor(big, 32));
   const uint32_t e = __float_as_uint(big) >> 23;
-  down = __uint_as_float((254u - min(e, 253u)) << 23);
-  unit = 1.f / sqrtf(sum + kNormEps);
-}
-
-// Eight bf16 times a power of two, in fp16
-__device__ __forceinline__ f16x8 scaled_half(bf16x8 raw, float down) {
-  const u32x4 x = __builtin_bit_cast(u32x4, raw);
-  u32x4 o;
+  const float down = __uint_as_float((254u - min(e, 253u)) << 23);
+  float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{bf16_lo(x[i]) * down, bf16_hi(x[i]) * down}), f16x2));
-  return __builtin_bit_cast(f16x8, o);
+  for (int s = 0; s < 4; ++s) {
+    const u32x4 x = __builtin_bit_cast(u32x4, row[s]);
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 f = {bf16_lo(x[i]) * down, bf16_hi(x[i]) * down};
+      sum = fmaf(f[0], f[0], sum);
+      sum = fmaf(f[1], f[1], sum);
+      o[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
+    }
+    half[s] = __builtin_bit_cast(f16x8, o);
+  }
+  sum += __shfl_xor(sum, 16);
+  sum += __shfl_xor(sum, 32);
+  // (beyond 2^40 the sum is nothing beside 1e-6 down^2, which may pass fp32)
+  const bool small = down > 0x1p40f;
+  unit = 1.f / sqrtf(small ? kNormEps : sum + kNormEps * down * down) * (small ? __uint_as_float(e << 23) : 1.f);
 }
 
 template <int NP>
@@ -191,16 +195,16 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(GdrParams p, GdrLayout lay
   // rows of K and Q as operands: lane l row l % 16 of tile w, channels 32 s + 8
   // (l / 16); rows behind the end repeat the last one, with factors of 0
   // (every load of the workgroup's inputs is issued before the first is used)
-  bf16x8 kf[4], qf[4];
+  bf16x8 kraw[4], qraw[4];
   const int r0 = 16 * w + l16;
   {
     const int64_t t = t0 + min(r0, len - 1);
     const uint16_t* kp = p.k + t * p.k_t + hk * p.k_h + 8 * g4;
     const uint16_t* qp = p.q + t * p.q_t + hk * p.q_h + 8 * g4;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) kf[s] = *reinterpret_cast<const bf16x8*>(kp + 32 * s);
+    for (int s = 0; s < 4; ++s) kraw[s] = *reinterpret_cast<const bf16x8*>(kp + 32 * s);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) qf[s] = *reinterpret_cast<const bf16x8*>(qp + 32 * s);
+    for (int s = 0; s < 4; ++s) qraw[s] = *reinterpret_cast<const bf16x8*>(qp + 32 * s);
   }
   const int64_t tg = t0 + min(lane, len - 1);  // gates: lane = token
   const uint16_t raw_a = p.a[tg * p.a_t + h * p.a_h], raw_beta = p.beta[tg * p.b_t + h * p.b_h];
@@ -216,24 +220,23 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(GdrParams p, GdrLayout lay
     L.G[lane] = G;
     L.beta[lane] = lane < len ? gdr_sigmoid(bf16_to_f32(raw_beta)) : 0.f;
   }
+  f16x8 kf[4], qf[4];
   {
-    float rk, rq, kd, qd;
-    row_factors(kf, rk, kd);
-    row_factors(qf, rq, qd);
+    float rk, rq;
+    scale_row(kraw, kf, rk);
+    scale_row(qraw, qf, rq);
 #pragma unroll
     for (int s = 0; s < 4; ++s) L.kf[w][s][lane] = kf[s];
     if (first) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        units[(4 * w + s) * 64] = scaled_half(kf[s], kd);
-        units[(kKUnits + 4 * w + s) * 64] = scaled_half(qf[s], qd);
+        units[(4 * w + s) * 64] = kf[s];
+        units[(kKUnits + 4 * w + s) * 64] = qf[s];
       }
     }
     if (g4 == 0) {
       L.rk[r0] = r0 < len ? rk : 0.f;
       L.rq[r0] = r0 < len ? rq : 0.f;
-      L.kd[r0] = kd;
-      L.qd[r0] = qd;
     }
   }
   __syncthreads();
@@ -241,7 +244,7 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(GdrParams p, GdrLayout lay
   // of row l % 16 of tile r (see scan_kernel), tokens 32 z + 4 (l / 16) .. + 3
   // and 16 further on
   if (first) {
-    const uint16_t* kl = reinterpret_cast<const uint16_t*>(&L.kf[0][0][0]);
+    const _Float16* kl = reinterpret_cast<const _Float16*>(&L.kf[0][0][0]);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int unit = 4 * w + u, r = unit >> 1;
@@ -251,16 +254,14 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(GdrParams p, GdrLayout lay
       for (int j = 0; j < 8; ++j) {
         // token t's channel c: tile t / 16, k-step c / 32, lane t % 16 + 16 (c / 8 % 4)
         const int tile = 2 * (unit & 1) + (j >> 2), row = 4 * g4 + (j & 3);
-        const uint16_t k = kl[((tile * 4 + (c >> 5)) * 64 + row + 16 * ((c >> 3) & 3)) * 8 + (c & 7)];
-        e[j] = (_Float16)(bf16_to_f32(k) * L.kd[16 * tile + row]);
+        e[j] = kl[((tile * 4 + (c >> 5)) * 64 + row + 16 * ((c >> 3) & 3)) * 8 + (c & 7)];
       }
       units[(2 * kKUnits + unit) * 64] = e;
     }
   }
   const double Gend = L.G[kC - 1];  // tokens behind the end add nothing
   if (tid < kC) {
-    const float eG = ex2(float(L.G[tid])), b = L.beta[tid], kd = L.kd[tid], qd = L.qd[tid];
-    const float rk = L.rk[tid] / kd, rq = L.rq[tid] / qd;  // powers of two: exact
+    const float eG = ex2(float(L.G[tid])), b = L.beta[tid], rk = L.rk[tid], rq = L.rq[tid];
     float* co = reinterpret_cast<float*>(p.ws + lay.coef) + (size_t(slot) * p.Hv + h) * kCoefs + tid;
     co[kBeta * kC] = b;
     co[kKs * kC] = b * eG * rk;
@@ -275,7 +276,7 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(GdrParams p, GdrLayout lay
     qk[j] = f32x4{};
     if (j <= w) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) qk[j] = mfma32(qf[s], L.kf[j][s][lane], qk[j]);
+      for (int s = 0; s < 4; ++s) qk[j] = mfma32h(qf[s], L.kf[j][s][lane], qk[j]);
     }
   }
   __builtin_amdgcn_sched_barrier(0);
@@ -284,7 +285,7 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(GdrParams p, GdrLayout lay
     kk[j] = f32x4{};
     if (j <= w) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) kk[j] = mfma32(kf[s], L.kf[j][s][lane], kk[j]);
+      for (int s = 0; s < 4; ++s) kk[j] = mfma32h(kf[s], L.kf[j][s][lane], kk[j]);
     }
   }
   __syncthreads();  // kf is read: A takes its place

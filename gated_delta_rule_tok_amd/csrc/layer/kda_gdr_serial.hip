@@ -78,15 +78,25 @@ __global__ __launch_bounds__(256) void serial_kernel(GdrParams p) {
     }
     const float decay = expf(gdr_log_decay(bf16_to_f32(p.a[t * p.a_t + h * p.a_h]), A_log, dt_bias));
     const float beta = gdr_sigmoid(bf16_to_f32(p.beta[t * p.b_t + h * p.b_h]));
-    const float k0 = bf16_lo(kw), k1 = bf16_hi(kw), q0 = bf16_lo(qw), q1 = bf16_hi(qw);
-    float kk = k0 * k0 + k1 * k1, qq = q0 * q0 + q1 * q1, qk = q0 * k0 + q1 * k1;
+    float k0 = bf16_lo(kw), k1 = bf16_hi(kw), q0 = bf16_lo(qw), q1 = bf16_hi(qw);
+    float kk, qq, qk;
+    const auto sums = [&] {
+      kk = k0 * k0 + k1 * k1, qq = q0 * q0 + q1 * q1, qk = q0 * k0 + q1 * k1;
 #pragma unroll
-    for (int o = 32; o; o >>= 1) {
-      kk += __shfl_xor(kk, o);
-      qq += __shfl_xor(qq, o);
-      qk += __shfl_xor(qk, o);
+      for (int o = 32; o; o >>= 1) {
+        kk += __shfl_xor(kk, o);
+        qq += __shfl_xor(qq, o);
+        qk += __shfl_xor(qk, o);
+      }
+    };
+    sums();
+    float ke = kNormEps, qe = kNormEps;
+    if (fmaxf(kk, qq) > 0x1p100f) {  // (the same in every lane) squares that fp32 may not hold
+      if (kk > 0x1p100f) k0 *= 0x1p-70f, k1 *= 0x1p-70f, ke = 0.f;  // 1e-6 2^-140 is nothing beside them
+      if (qq > 0x1p100f) q0 *= 0x1p-70f, q1 *= 0x1p-70f, qe = 0.f;
+      sums();
     }
-    const float rk = 1.f / sqrtf(kk + kNormEps), rq = 1.f / sqrtf(qq + kNormEps);
+    const float rk = 1.f / sqrtf(kk + ke), rq = 1.f / sqrtf(qq + qe);
     qk *= rk * rq;
     *reinterpret_cast<float2*>(&kq[wave][0][2 * lane]) = float2{k0 * rk, k1 * rk};
     *reinterpret_cast<float2*>(&kq[wave][1][2 * lane]) = float2{q0 * rq, q1 * rq};

@@ -330,6 +330,23 @@ def test_keys_and_queries_of_any_size(size):
     _check_gdr(x, [(0, 200)], out, fin, _reference(x, [(0, 200)], None), torch.float32, f"keys times {size}")
 
 
+@pytest.mark.parametrize("state", ["float32", "bfloat16"])
+@pytest.mark.parametrize("lens", [[200], [7], [2100]], ids=str)
+@pytest.mark.parametrize("size", [1e-35, 1e10, 1e19, 1e37])
+def test_rows_of_keys_and_queries_of_any_size(size, lens, state):
+    """Rows whose squares fp32 does not hold, among ordinary ones and next to each other."""
+    import torch
+    dtype = getattr(torch, state)
+    x = Gdr(lens[0], 1, 2, seed=21)
+    x.k[1::3] *= size
+    x.k[2::6] *= size
+    x.q[2::5] *= size
+    x.q[1] *= size
+    s0 = _state((1, 2, D, D), dtype, 11)
+    out, fin = _prefill(x, lens, dtype, s0)
+    _check_gdr(x, _spans(lens), out, fin, _reference(x, _spans(lens), s0), dtype, f"rows times {size}")
+
+
 def test_zero_rows():
     """Keys and queries of zeros have norm 1e-3: no division by zero, and no update."""
     import torch
@@ -416,6 +433,21 @@ def test_decode(n, hk, hv, state):
     rest = torch.ones(n + 7, dtype=torch.bool, device="cuda")
     rest[slots] = False
     assert torch.equal(pool[rest], before[rest])
+
+
+def test_decode_of_large_keys_and_queries():
+    import torch
+    x = Gdr(9, 1, 2, seed=22)
+    x.k[:3] *= 1e37
+    x.q[2:5] *= 1e19
+    x.k[6] *= 1e18
+    x.q[6] *= 1e-20
+    pool = _state((9, 2, D, D), torch.float32, 12)
+    before = pool.clone()
+    out = torch.zeros(9, 2, D, dtype=torch.bfloat16, device="cuda")
+    _kda().kda_gdr_decode_step(*x.rows(), pool, torch.arange(9, dtype=torch.int32, device="cuda"), out)
+    spans = _spans([1] * 9)
+    _check_gdr(x, spans, out, pool, _reference(x, spans, before), torch.float32, "decode, large keys")
 
 
 def test_prefill_then_decode_is_a_longer_prefill():
