@@ -7,11 +7,14 @@
 
 namespace kda {
 
-// log a = -exp(A_log) softplus(x + dt_bias), not below -120: e^-120 is 0 in
-// fp32, and a sum of 64 stays finite.  A NaN stays one.
+// log a = -exp(A_log) softplus(x), x = a + dt_bias, not below -120: e^-120 is 0
+// in fp32, and a sum of 64 stays finite.  Above A_log = 88, where its exponential
+// passes fp32, the excess c goes to x: exp(A_log) e^x = e^88 e^(x + c), softplus
+// is e^x below -20, and from there on the product is beyond 120 either way.  A
+// NaN stays one.
 static __device__ __forceinline__ float gdr_log_decay(float a, float A_log, float dt_bias) {
-  const float x = a + dt_bias;
-  const float l = -expf(A_log) * (fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))));
+  const float c = fmaxf(A_log - 88.f, 0.f), x = a + dt_bias + c;
+  const float l = -expf(A_log - c) * (fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))));
   return l < -120.f ? -120.f : l;
 }
 

@@ -261,6 +261,20 @@ def test_decays_of_every_size(lens):
     _check_gdr(x, _spans(lens), out, fin, _reference(y, _spans(lens), s0), torch.float32, f"decays {lens}")
 
 
+@pytest.mark.parametrize("lens", [[150], [7]], ids=str)
+def test_decay_rates_of_any_size(lens):
+    """exp(A_log) beyond fp32 times a softplus below it: a finite decay."""
+    import torch
+    x = Gdr(lens[0], 1, 4, seed=23)
+    x.A_log = torch.tensor([90.0, 120.0, 87.0, -120.0], device="cuda")
+    x.dt_bias = torch.zeros(4, device="cuda")
+    rate = torch.tensor([[-95.0, -127.0, -92.0, 100.0], [-112.0, -200.0, -100.0, 3e38]], device="cuda")
+    x.a = rate[torch.arange(lens[0], device="cuda") % 2].bfloat16()
+    s0 = _state((1, 4, D, D), torch.float32, 13)
+    out, fin = _prefill(x, lens, torch.float32, s0)
+    _check_gdr(x, _spans(lens), out, fin, _reference(x, _spans(lens), s0), torch.float32, f"rates {lens}")
+
+
 def test_keys_of_one_direction():
     """Nearly equal keys and hardly any decay: the triangle is far from the identity."""
     import torch
