@@ -13,6 +13,8 @@
 // and one step of refinement.  t and n are exact without a residual (two 8-bit
 // factors and 7 * 2^6), and a quotient half way between two e4m3 values is then
 // found as such and goes to the even one.
+//
+// Rows of any finite size are taken: see where var is formed.
 #include "kda_layer_internal.h"
 #include "kda_mfma.h"
 
@@ -81,7 +83,7 @@ __device__ __forceinline__ float block_reduce(float v, float* red) {
 
 template <int VPT, bool VEC, bool RES, bool FP8>
 __global__ __launch_bounds__(1024) void norm_kernel(NormParams np) {
-  __shared__ float red[2][16];
+  __shared__ float red[3][16];
   const int t = threadIdx.x;
   const int64_t row = int64_t(blockIdx.y) * kGridX + blockIdx.x;
   if (row >= np.rows) return;
@@ -108,7 +110,24 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams np) {
     for (int j = 0; j < 8; ++j) sum = fmaf(s[i][j], s[i][j], sum);
   }
   sum = block_reduce<false>(sum, red[0]);
-  const float rstd = 1.f / sqrtf(sum / float(np.dim) + np.eps);
+  // Squares that fp32 may not hold (the same for the whole row): the row times a
+  // power of two, which leaves y as it is.  2^-80 brings its largest element, 2^50
+  // at least, to 2^-30 .. 2^48; 2^70 brings the least bf16 to 2^-63 and, where eps
+  // counts, keeps eps times its square below 2^60.
+  float var = sum / float(np.dim) + np.eps;
+  if (var > 0x1p100f || var < 0x1p-80f) {
+    const float p = var > 1.f ? 0x1p-80f : 0x1p70f;
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[i][j] *= p;
+        sum = fmaf(s[i][j], s[i][j], sum);
+      }
+    var = block_reduce<false>(sum, red[1]) / float(np.dim) + np.eps * p * p;
+  }
+  const float rstd = var == 0.f ? 0.f : 1.f / sqrtf(var);  // a row of zeros without eps: zeros
   if (!FP8) {
     uint16_t* o = static_cast<uint16_t*>(np.out) + row * np.o_row;
 #pragma unroll
@@ -141,7 +160,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams np) {
     float a = m[0];
 #pragma unroll
     for (int i = 1; i < VPT; ++i) a = fmaxf(a, m[i]);
-    a = block_reduce<true>(a, red[1]);
+    a = block_reduce<true>(a, red[2]);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) m[i] = a;
   }

@@ -152,9 +152,10 @@ typedef enum { KDA_OUT_BF16 = 0, KDA_OUT_E4M3 = 1 } kda_out_dtype_t;
  *
  * with one scale per row (group_size 0) or per group_size = 128 channels (the
  * last group of a row may be shorter).  A group that is zero throughout gets
- * scale 0 and zeros.  y is formed from the unrounded s.  Sums are fp32: a row
- * whose sum of squares passes 3e38 gives zeros, one with an infinity or a NaN
- * gives NaN (NaN scales).
+ * scale 0 and zeros, a row of zeros zeros (eps = 0 included).  y is formed from
+ * the unrounded s.  Sums are fp32, of a scaled row where squares would leave its
+ * range: finite s of any size are taken.  A row with an infinity or a NaN gives
+ * NaN (NaN scales).
  *
  *   x, residual  bf16 [num_rows, dim], rows x_row and residual_row elements
  *                apart, dim contiguous

@@ -590,6 +590,31 @@ def test_norm_of_zeros_and_of_what_is_not_finite():
     assert b[3].isnan().all()
 
 
+@pytest.mark.parametrize("out", ["bf16", "rows", "groups"])
+@pytest.mark.parametrize("dim", [100, 512, 2056, 16391])
+@pytest.mark.parametrize("size,eps", [(1e20, 1e-6), (1e37, 0.0), (1e-20, 0.0), (1e-30, 0.0), (1e-15, 1e-30)])
+def test_norm_of_rows_of_any_size(size, eps, dim, out):
+    """Rows whose sum of squares fp32 does not hold, either way, and a row of zeros without eps."""
+    import torch
+    fp8 = out != "bf16"
+    group = 128 if out == "groups" else 0
+    for residual in (False, True):
+        x, r, w = _norm_inputs(4, dim, dim + 9, residual=residual)
+        x = x * size
+        x[2] = 0
+        if residual:
+            r = r * size
+            r[2] = 0
+        ra = r.clone() if residual else None
+        o = torch.empty(4, dim, dtype=torch.float8_e4m3fn if fp8 else torch.bfloat16, device="cuda")
+        sc = torch.full((4, -(-dim // 128) if group else 1), -1.0, device="cuda") if fp8 else None
+        _kda().kda_add_rms_norm(x, ra, w, eps, o, sc, group)
+        rows = [0, 1, 3]
+        _check_norm(x[rows], r[rows] if residual else None, w, ra[rows] if residual else None, o[rows],
+                    sc[rows] if fp8 else None, group, f"{size} {dim} {out}", eps=eps)
+        assert not o[2].float().any() and not (fp8 and sc[2].any())
+
+
 def test_norm_of_many_rows():
     """More rows than one row of the grid holds (2^20)."""
     import torch
