@@ -173,7 +173,8 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams np) {
       np.scale[row * groups + (np.group ? c >> 7 : 0)] = m[i] * rstd / kFp8Max;
     // a power of two keeps 448 t and 1 / m in range; a group of zeros is divided by one
     const float p2 = m[i] < 0x1p-60f ? 0x1p60f : m[i] > 0x1p60f ? 0x1p-60f : 1.f;
-    const float d = m[i] > 0.f ? m[i] * p2 : 1.f, inv = 1.f / d, k = kFp8Max * p2;
+    const float d = m[i] > 0.f ? m[i] * p2 : 1.f, inv = 1.f / d;
+    const float k = rstd == 0.f ? 0.f : kFp8Max * p2;  // (beside an infinity: zeros, as in bf16)
     float z[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {

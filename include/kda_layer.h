@@ -154,8 +154,10 @@ typedef enum { KDA_OUT_BF16 = 0, KDA_OUT_E4M3 = 1 } kda_out_dtype_t;
  * last group of a row may be shorter).  A group that is zero throughout gets
  * scale 0 and zeros, a row of zeros zeros (eps = 0 included).  y is formed from
  * the unrounded s.  Sums are fp32, of a scaled row where squares would leave its
- * range: finite s of any size are taken.  A row with an infinity or a NaN gives
- * NaN (NaN scales).
+ * range: finite s of any size are taken.  Where s is infinite y is NaN, and 0 in
+ * the rest of its row; in e4m3 the scale over an infinity is NaN, and groups
+ * beside it get scale 0 and zeros.  A NaN makes its row's bf16 output, or all of
+ * its row's scales, NaN.
  *
  *   x, residual  bf16 [num_rows, dim], rows x_row and residual_row elements
  *                apart, dim contiguous

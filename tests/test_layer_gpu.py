@@ -615,6 +615,29 @@ def test_norm_of_rows_of_any_size(size, eps, dim, out):
         assert not o[2].float().any() and not (fp8 and sc[2].any())
 
 
+@pytest.mark.parametrize("dim", [300, 2048, 2056])
+def test_norm_of_infinities(dim):
+    """What the formula gives: NaN in the place of an infinity, zeros beside it;
+    in e4m3 a NaN scale for its group and scales and codes of zero for the others."""
+    import torch
+    x, _, w = _norm_inputs(3, dim, 43, residual=False)
+    x = x.contiguous()
+    x[0, 5] = float("inf")
+    x[2, 5] = float("-inf")
+    b = torch.empty(3, dim, dtype=torch.bfloat16, device="cuda")
+    _kda().kda_add_rms_norm(x, None, w, 1e-6, b)
+    o = torch.empty(3, dim, dtype=torch.float8_e4m3fn, device="cuda")
+    sc, sr = torch.empty(3, -(-dim // 128), device="cuda"), torch.empty(3, 1, device="cuda")
+    _kda().kda_add_rms_norm(x, None, w, 1e-6, o, sc, 128)
+    for i in (0, 2):
+        assert b[i, 5].isnan() and not b[i, :5].any() and not b[i, 6:].any()
+        assert sc[i, 0].isnan() and not sc[i, 1:].any() and not o[i, 128:].float().any()
+    _check_norm(x[1:2], None, w, None, o[1:2], sc[1:2], 128, "beside infinities")
+    _kda().kda_add_rms_norm(x, None, w, 1e-6, o, sr)
+    assert sr[0].isnan() and sr[2].isnan()
+    _check_norm(x[1:2], None, w, None, o[1:2], sr[1:2], 0, "beside infinities")
+
+
 def test_norm_of_many_rows():
     """More rows than one row of the grid holds (2^20)."""
     import torch
