@@ -3,13 +3,14 @@
 //
 // Bound by the weights' bytes (each is used for at most 64 tokens), so the
 // kernel streams w in 16-byte loads, one pass, and feeds 16x16x32 bf16 MFMAs:
-// A = 16 tokens, B = 16 rows of w.  A nibble q becomes the bf16 number 128 + q
-// by an OR with 0x4300 (exact: bf16 steps by 1 there), two at a time, and the
-// group's sum is corrected in fp32:
+// A = 16 tokens, B = 16 rows of w.  A nibble q becomes the bf16 number (128 + q)
+// 2^-15 by an OR with the bits of 2^-8 (exact: bf16 steps by 2^-15 there), two at
+// a time, and the group's sum is corrected in fp32:
 //   sum (q - z) x = sum (128 + q) x - (128 + z) sum x,
-// with sum x from one more MFMA against ones, shared by all rows of w.  x
+// with sum x from one more MFMA against 2^-15, shared by all rows of w.  x
 // stays bf16 and every product is exact in fp32; scales are applied to the
-// group's fp32 sum.
+// group's fp32 sum, and 2^15 to the last one.  That power costs nothing and
+// keeps 143 |x| summed over a group inside fp32 for every finite x.
 //
 // A lane's 16 bytes are 32 adjacent k of one row (lane l: row l % 16, k from
 // 32 (l / 16)); two swaps of lane halves and two of lane rows transpose the
@@ -113,11 +114,11 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Params p) {
 #pragma unroll
       for (int j = 0; j < RQ; ++j) b.x[i][j] = *reinterpret_cast<const u32x4*>(xk + (xrow[i][j] + xp));
   };
-  // 128 in both halves, in a vector register: an instruction reads one scalar
+  // 2^-8 in both halves, in a vector register: an instruction reads one scalar
   // only, so that two literals would make (q & m) | e two instructions
-  uint32_t e128 = 0x43004300u;
+  uint32_t e128 = 0x3b803b80u;
   asm("" : "+v"(e128));
-  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x38003800u, 0x38003800u, 0x38003800u, 0x38003800u});  // 2^-15
   f32x4 acc[MT][NT] = {};
   const auto add = [&](B& b, int blk, int seg) {
     // x through LDS into operands: a load of it takes whole lines of 4 rows, where loads
@@ -218,7 +219,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Params p) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int m = m0 + 16 * (i / NT) + 4 * g4 + r;
-      if (m < p.M && n < p.N) p.y[size_t(m) * p.y_row + n] = f32_to_bf16(y[r]);
+      if (m < p.M && n < p.N) p.y[size_t(m) * p.y_row + n] = f32_to_bf16(y[r] * 0x1p15f);
     }
   }
 }

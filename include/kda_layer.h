@@ -191,10 +191,12 @@ kda_status_t kda_add_rms_norm(const void* x, void* residual, const void* weight,
  *
  * group_size is 32, 64 or 128, k a positive multiple of it (at most 2^20),
  * 1 <= n <= 2^24, 0 <= num_tokens <= 64; x and w are 16-byte aligned.  Sums
- * are fp32, of exact products.  A value of x that is not finite makes its row
- * of y NaN; other rows are not affected.  A token's sums may be taken in
- * another order in a call with another number of tokens.  No workspace.  x may
- * be NULL when num_tokens is 0.
+ * are fp32, of exact products; a group's is formed as sum (128 + w) x - (128 + z)
+ * sum x, which costs about five of the sum's 24 bits.  Sums up to 2^143 are held
+ * on the way to y, and so is every finite x (z from 0 to 15).  A value of x that
+ * is not finite makes its row of y NaN; other rows are not affected.  A token's
+ * sums may be taken in another order in a call with another number of tokens.
+ * No workspace.  x may be NULL when num_tokens is 0.
  */
 kda_status_t kda_w4_proj(const void* x, const void* w, const void* scales, const void* zeros,
                          void* y, void* stream, int32_t num_tokens, int32_t k, int32_t n,

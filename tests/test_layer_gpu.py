@@ -724,6 +724,20 @@ def test_w4_rows_do_not_mix():
     assert y2[3].isnan().all() and torch.equal(y2[4:], y[4:]) and torch.equal(y2[:3], y[:3])
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("m,k,n,group", [(1, 512, 100, 128), (16, 160, 33, 32), (40, 512, 4200, 64)])
+@pytest.mark.parametrize("size", [1e-30, 1e30, 1e37, 3e38])
+def test_w4_of_values_of_any_size(size, m, k, n, group, zeros):
+    """Sums of 143 |x| beyond fp32 whose result is not."""
+    import torch
+    x, w, s, z = _w4_inputs(m, k, n, group, zeros, 53)
+    x = (x.clamp(-1, 1) * size).bfloat16()
+    s = s * 2.0 ** -12
+    y = torch.full((m, n), float("nan"), dtype=torch.bfloat16, device="cuda")
+    _kda().kda_w4_proj(x, w, s, z, y, group)
+    _w4_check(x, w, s, z, group, y, f"{size} {m}x{k}x{n}")
+
+
 # ---- together ---------------------------------------------------------------
 
 class Layer:
