@@ -82,7 +82,8 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Params p) {
   const int n0 = blockIdx.x * (16 * NT), m0 = blockIdx.y * (16 * MT);
   const int groups = p.K / G, blocks = (p.K + 127) / 128;
   // rows behind the last row or token repeat it: their sums are not stored
-  // (32-bit offsets from scalar bases: 64 rows of at most 2^19 bytes of w, and of 2^20 elements of x)
+  // (32-bit offsets from scalar bases: 32 rows of at most 2^19 bytes of w, 64 of x at most 2^24
+  // elements apart)
   const uint8_t* wbase = p.w + size_t(n0) * (p.K / 2);
   uint32_t wrow[NT], xrow[MT][RQ];
   const int last = p.K % 128 ? p.K - p.K % 128 : p.K;  // where a block that is not whole begins
@@ -168,7 +169,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Params p) {
       }
     }
   };
-  // Segments of 256 groups, whose scales and zeros go through LDS (one per row
+  // Segments of kSegGroups groups, whose scales and zeros go through LDS (one per row
   // and group straight into registers took longer than the weights: 16 lines
   // per load of 2 bytes).  A wave's blocks of a segment are adjacent.  Every
   // load is unconditional (the last block is repeated behind the end), so that
@@ -257,7 +258,8 @@ hipError_t launch(const W4Params& p, hipStream_t st) {
 // own that read w again (64 x 7168 x 1536 10.5 us against 20.4 with all 64 in
 // one, 24 x 7168 x 7168 17.0 against 18.5 with 32), but more than 32 with many
 // rows of w in one (61 x 2048 x 7171 12.4 against 17.8, 64 x 7168 x 7168 30.6
-// against 33.0).
+// against 33.0).  (That form's variants for groups of 64 spill 12 and 13 of their
+// 256 registers; none of the others spills.)
 hipError_t launch_w4(const W4Params& p, int cus, hipStream_t stream) {
   const int64_t wide = (p.N + 31) / 32, tiles = (p.M + 15) / 16;
   if (p.M <= 4)

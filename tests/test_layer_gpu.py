@@ -738,6 +738,20 @@ def test_w4_of_values_of_any_size(size, m, k, n, group, zeros):
     _w4_check(x, w, s, z, group, y, f"{size} {m}x{k}x{n}")
 
 
+def test_w4_rows_do_not_depend_on_the_tokens_beside():
+    """At one number of tokens, where each wave sums several blocks of k."""
+    import torch
+    for m in (3, 16, 40):
+        x, w, s, z = _w4_inputs(m, 7168, 70, 64, True, 54)
+        y = torch.empty(m, 70, dtype=torch.bfloat16, device="cuda")
+        _kda().kda_w4_proj(x, w, s, z, y, 64)
+        x2 = torch.randn(m, 7168, generator=_gen(55), device="cuda").bfloat16()
+        x2[1] = x[1]
+        y2 = torch.empty_like(y)
+        _kda().kda_w4_proj(x2, w, s, z, y2, 64)
+        assert torch.equal(y[1], y2[1])
+
+
 # ---- together ---------------------------------------------------------------
 
 class Layer:
