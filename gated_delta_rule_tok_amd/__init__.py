@@ -473,14 +473,24 @@ def kda_gate_proj(hidden, w_ab, w_b, p_ab, g, workspace, stream=None) -> None:
 
 def _torch():
     """torch, imported on first use (like load_library)."""
-    global _torch_module
+    global _torch_module, _raw_stream, _device
     if _torch_module is None:
         import torch
+        _raw_stream, _device = _queries(torch)
         _torch_module = torch
     return _torch_module
 
 
-_torch_module = None
+def _queries(torch):
+    """(handle of the current stream of GPU i, index of the current GPU) as
+    functions: torch's own short forms of the public calls, 1.2 us less per call,
+    and the public ones in a torch that does not have them."""
+    c, cuda = torch._C, torch.cuda
+    return (getattr(c, "_cuda_getCurrentRawStream", None) or (lambda i: cuda.current_stream(i).cuda_stream),
+            getattr(c, "_cuda_getDevice", None) or cuda.current_device)
+
+
+_torch_module = _raw_stream = _device = None
 
 
 def _refuse(t, name, dtype, shape, index):
@@ -531,10 +541,10 @@ def _gpu(t, name):
 def _call(name, fn, index, stream, before, after):
     """fn(*before, stream, *after) on GPU `index`; raises on a refusal."""
     if stream is None:
-        stream = _torch_module._C._cuda_getCurrentRawStream(index)
+        stream = _raw_stream(index)
     elif isinstance(stream, _torch_module.cuda.Stream):
         stream = stream.cuda_stream
-    if index == _torch_module._C._cuda_getDevice():
+    if index == _device():
         rc = fn(*before, stream, *after)
     else:
         with _torch_module.cuda.device(index):

@@ -154,3 +154,13 @@ def test_binding_rejects_host_tensors():
         kda.kda_w4_proj(x, torch.zeros(3, 32, dtype=torch.uint8), x, None, x, 32)
     with pytest.raises(TypeError):
         kda.kda_add_rms_norm(None, None, None, 1e-6, None)
+
+
+def test_stream_and_device_queries():
+    """The short forms where torch has them, the public calls where it does not."""
+    from types import SimpleNamespace as N
+    raw, device = kda._queries(N(_C=N(_cuda_getCurrentRawStream="r", _cuda_getDevice="d"), cuda=N()))
+    assert raw == "r" and device == "d"
+    cuda = N(current_stream=lambda i: N(cuda_stream=100 + i), current_device=lambda: 3)
+    raw, device = kda._queries(N(_C=N(), cuda=cuda))
+    assert raw(2) == 102 and device() == 3
