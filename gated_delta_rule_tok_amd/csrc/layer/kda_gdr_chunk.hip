@@ -15,13 +15,14 @@
 // scan_kernel walks the chunks of a sequence with the state in registers.
 //
 // What bounds it.  A chunk depends on the one before, 4 us with an fp32 state;
-// 8 x 2048 tokens, 16 heads, fp32 state: prep 68 us, scan 136 us (medians of a
-// trace; 219 MB of inputs and outputs: 43 us at the rate of a copy).  With more
+// 8 x 2048 tokens, 16 heads, fp32 state: prep 71 us, scan 142 us (medians of a
+// trace, which vary by 5% from one to the next; 219 MB of inputs and outputs: 43 us at the rate of a copy).  With more
 // states than compute units it is the bytes too: 32 ragged prompts, 32 heads,
-// bf16 state, prep 222 us and scan 283 us for 1.7 GB, the operands that prep
+// bf16 state, prep 228 us and scan 285 us for 1.7 GB, the operands that prep
 // writes and scan reads among them.
 //
-// Precision.  Operands are fp16 (11 bits), sums fp32.
+// Precision.  Operands are fp16 (11 bits), sums fp32; prep_kernel spills three
+// registers.
 //  * A row of K or Q, times a power of two that brings its largest element to
 //    [1, 2), is exact in fp16 (bf16 has 8 bits; elements below 2^-14 of the
 //    largest are off by 2^-25 of it at most).  Norms, decays and the powers of

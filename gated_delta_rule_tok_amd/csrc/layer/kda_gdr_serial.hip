@@ -9,7 +9,7 @@
 // (o from the old state, so that k and q share one reduction and one barrier).
 // A decode step is bound by the state's bytes, read and written once: every
 // load of the state is issued before anything else, 16 bytes per lane, 32 KB in
-// flight per workgroup.  256 sequences x 16 heads, fp32: 110 us, 4.9 TB/s (a
+// flight per workgroup.  256 sequences x 16 heads, fp32: 111 us, 4.8 TB/s (a
 // copy reaches 5.1).
 #include "kda_gdr.h"
 
@@ -172,9 +172,9 @@ hipError_t launch_gdr_serial(const GdrParams& p, hipStream_t stream) {
   void* args[] = {&arg};
   const int64_t pairs = int64_t(p.N) * p.Hv;
   // Columns per workgroup: few states are spread over more workgroups (1 x 16:
-  // 4.2 us with 32 columns, 4.9 with 128), a bf16 state of 64 columns is too
-  // little for one (128 x 32: 60 us against 57 with 128; fp32 256 x 16: 108.6
-  // against 110.8).
+  // 4.9 us with 32 columns, 5.0 with 64, 5.6 with 128; 256 x 16, fp32, 114, 111
+  // and 110), a bf16 state of 64 columns is too little for one (128 x 32: 61 us
+  // against 58 with 128, 93 with 32).
   const int cols = pairs <= 64 ? 32 : p.state_bf16 && pairs >= 512 ? 128 : 64;
   const void* f = cols == 32   ? (p.state_bf16 ? reinterpret_cast<const void*>(&serial_kernel<true, 32>)
                                                : reinterpret_cast<const void*>(&serial_kernel<false, 32>))

@@ -216,7 +216,7 @@ hipError_t launch(const NormParams& p, hipStream_t st) {
 
 // Pieces of a row per thread: one for few rows (latency), two for many (a
 // reduction over half the waves): 1 x 7168 3.0 us with one, 3.4 with four; 4096
-// x 2048 12.1 / 11.4 us with one / two, 16384 x 7168 to e4m3 154 / 149 us (5.5
+// x 2048 12.1 / 11.4 us with one / two, 16384 x 7168 to e4m3 154 / 150 us (5.5
 // TB/s; a copy reaches 5.1), 16384 x 5120 118 / 120.
 template <bool VEC>
 hipError_t pick(const NormParams& p, hipStream_t st) {
