@@ -100,9 +100,9 @@ size_t kda_gdr_get_workspace_size(int64_t max_tokens, int32_t key_heads, int32_t
  * a bf16 state (out, which is bf16, 11 bits either way), relative to the
  * largest element of their column, so that out is off by a share of scale times
  * the state, also where a query is far below 1e-3 and its row of out with it.
- * Finite q, k, v, gates and states of any size are taken, columns of a state as
- * long as fp32 holds their norm.  The final state and out are rounded once, at
- * the end.
+ * Finite q, k, v, gates and states of any size are taken, as long as fp32 holds
+ * the norm of a state's column and |scale| times it.  The final state and out are
+ * rounded once, at the end.
  * An input that is not finite makes the rows of its sequence and of the value
  * heads that read it undefined from its chunk of 64 tokens on, and their
  * final states; other sequences and heads are not affected.
