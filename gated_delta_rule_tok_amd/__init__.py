@@ -18,6 +18,12 @@ The operators around the forward (include/kda_layer.h) are here too:
     kda_add_rms_norm(x, residual, weight, 1e-6, hidden)
     kda_w4_proj(hidden, w, scales, None, qkvab, 128)
     kda_gdr_decode_step(q, k, v, a, beta_logits, A_log, dt_bias, scale, pool, slots, out)
+
+and those on microscaled 4-bit numbers (include/kda_mx4.h):
+
+    kda_mx4_quant(x, codes, scales)
+    kda_mx4_proj(codes, scales, w, w_scales, y)       # or (x, None, w, w_scales, y) for few rows
+    kda_mx4_moe(hidden, router, bias, w_up, s_up, w_down, s_down, out, ids, gates, ws)
 """
 from __future__ import annotations
 
@@ -30,7 +36,8 @@ __all__ = ["kda_get_workspace_size", "kda_chunk_prefill_fwd", "kda_status_string
            "kda_workspace_status",
            "kda_last_hip_error", "kda_debug_set_vsplit", "kda_debug_set_kernel", "kda_debug_set_segment", "kda_debug_segment_length", "kda_debug_two_workgroups", "kda_spec_decode_step", "kda_chunk_prefill_fwd_noalloc", "kda_gate_proj",
            "kda_gate_proj_workspace_size", "kda_gdr_get_workspace_size", "kda_gdr_prefill_fwd",
-           "kda_gdr_decode_step", "kda_add_rms_norm", "kda_w4_proj", "KdaError", "library_path", "load_library"]
+           "kda_gdr_decode_step", "kda_add_rms_norm", "kda_w4_proj", "kda_mx4_quant", "kda_mx4_dequant",
+           "kda_mx4_proj", "kda_mx4_moe_workspace_size", "kda_mx4_moe", "KdaError", "library_path", "load_library"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libkda.so")
@@ -126,6 +133,17 @@ def load_library():
         lib.kda_add_rms_norm.restype = ctypes.c_int
         lib.kda_w4_proj.argtypes = [P, P, P, P, P, P, I32, I32, I32, I32, I64, I64]
         lib.kda_w4_proj.restype = ctypes.c_int
+        lib.kda_mx4_quant.argtypes = [P, P, P, P, I64, I32, I64]
+        lib.kda_mx4_quant.restype = ctypes.c_int
+        lib.kda_mx4_dequant.argtypes = [P, P, P, P, I64, I32, I64]
+        lib.kda_mx4_dequant.restype = ctypes.c_int
+        lib.kda_mx4_proj.argtypes = [P, P, P, P, P, P, I64, I32, I32, I64, I64]
+        lib.kda_mx4_proj.restype = ctypes.c_int
+        lib.kda_mx4_moe_workspace_size.argtypes = [I32, I32, I32, I32, I32, I32]
+        lib.kda_mx4_moe_workspace_size.restype = SZ
+        lib.kda_mx4_moe.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I64,
+                                    I64, ctypes.c_int, I32, F, SZ]
+        lib.kda_mx4_moe.restype = ctypes.c_int
         lib.kda_status_string.argtypes = [ctypes.c_int]
         lib.kda_status_string.restype = ctypes.c_char_p
         lib.kda_last_hip_error.argtypes = []
@@ -729,3 +747,131 @@ def kda_w4_proj(x, w, scales, zeros, y, group_size: int, stream=None) -> None:
             _view(y, "y", bf, (m, n), dev))
     _call("kda_w4_proj", lib.kda_w4_proj, dev, stream, ptrs,
           (m, k, n, group_size, _row_stride(x, "x"), _row_stride(y, "y")))
+
+
+# ---- include/kda_mx4.h: microscaled 4-bit numbers ------------------------------
+
+def _mx4(codes, scales, names, shape, index):
+    """Device pointers of dense codes [..., k / 2] and scales [..., k / 32] of `shape` [..., k]."""
+    torch = _torch_module
+    *rows, k = shape
+    return (_on(codes, names[0], torch.uint8, (*rows, k // 2), index),
+            _on(scales, names[1], torch.uint8, (*rows, k // 32), index))
+
+
+def _columns(k, name):
+    if k % 32 or k <= 0:
+        raise ValueError(f"{name} must have a multiple of 32 columns, got {k}")
+
+
+def kda_mx4_quant(x, codes, scales, stream=None) -> None:
+    """Queue codes, scales <- x as microscaled 4-bit numbers (see
+    include/kda_mx4.h, kda_mx4_quant).
+
+    x [M, k] bf16, rows may be strided (by multiples of 8); codes [M, k / 2] and
+    scales [M, k / 32] uint8, dense.
+    """
+    lib = load_library()
+    dev = _gpu(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M, k], got {tuple(x.shape)}")
+    m, k = shape = x.shape
+    _columns(k, "x")
+    ptrs = (_view(x, "x", _torch_module.bfloat16, shape, dev),
+            *_mx4(codes, scales, ("codes", "scales"), shape, dev))
+    _call("kda_mx4_quant", lib.kda_mx4_quant, dev, stream, ptrs, (m, k, _row_stride(x, "x")))
+
+
+def kda_mx4_dequant(codes, scales, out, stream=None) -> None:
+    """Queue out <- the values of codes and scales (see include/kda_mx4.h,
+    kda_mx4_dequant).  Shapes as for kda_mx4_quant, out [M, k] bf16."""
+    lib = load_library()
+    dev = _gpu(out, "out")
+    if out.dim() != 2:
+        raise ValueError(f"out must be [M, k], got {tuple(out.shape)}")
+    m, k = shape = out.shape
+    _columns(k, "out")
+    ptrs = (*_mx4(codes, scales, ("codes", "scales"), shape, dev),
+            _view(out, "out", _torch_module.bfloat16, shape, dev))
+    _call("kda_mx4_dequant", lib.kda_mx4_dequant, dev, stream, ptrs, (m, k, _row_stride(out, "out")))
+
+
+def kda_mx4_proj(x, x_scales, w, w_scales, y, stream=None) -> None:
+    """Queue y = x w^T with microscaled 4-bit weights (see include/kda_mx4.h,
+    kda_mx4_proj).
+
+    x [M, k] bf16 with x_scales None (M <= 64, rows may be strided), or codes
+    [M, k / 2] with x_scales [M, k / 32]; w [n, k / 2] and w_scales [n, k / 32]
+    uint8; y [M, n] bf16, rows may be strided.
+    """
+    lib = load_library()
+    dev = _gpu(x, "x")
+    torch = _torch_module
+    if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("x and w must be 2-D tensors")
+    m, k = x.shape
+    n = w.shape[0]
+    if x_scales is None:
+        _columns(k, "x")
+        xp, xs, row = _view(x, "x", torch.bfloat16, (m, k), dev), None, _row_stride(x, "x")
+    else:
+        k *= 2
+        _columns(k, "x (of values)")
+        (xp, xs), row = _mx4(x, x_scales, ("x", "x_scales"), (m, k), dev), 0
+    ptrs = (xp, xs, *_mx4(w, w_scales, ("w", "w_scales"), (n, k), dev),
+            _view(y, "y", torch.bfloat16, (m, n), dev))
+    _call("kda_mx4_proj", lib.kda_mx4_proj, dev, stream, ptrs, (m, k, n, row, _row_stride(y, "y")))
+
+
+def kda_mx4_moe_workspace_size(max_tokens: int, k: int, inter: int, experts: int, shared: int,
+                               top_k: int) -> int:
+    return int(load_library().kda_mx4_moe_workspace_size(int(max_tokens), int(k), int(inter), int(experts),
+                                                         int(shared), int(top_k)))
+
+
+_SCORING = {"sigmoid": 0, "softmax": 1}
+
+
+def kda_mx4_moe(x, router, router_bias, w_up, w_up_scales, w_down, w_down_scales, out, expert_ids,
+                expert_gates, workspace, scoring: str = "sigmoid", renormalise: bool = True,
+                route_scale: float = 1.0, state_indices=None, stream=None) -> None:
+    """Queue a mixture-of-experts layer for at most 64 tokens (see
+    include/kda_mx4.h, kda_mx4_moe).
+
+    x, out [M, k] bf16, rows may be strided (by multiples of 8); router [E, k]
+    bf16; router_bias [E] fp32 or None; w_up [E + S, 2 inter, k / 2], w_down
+    [E + S, k, inter / 2] uint8 with their scales ([..., k / 32], [..., inter /
+    32]), the last S experts shared by every token; expert_ids int32 and
+    expert_gates fp32 [M, top_k], written; workspace uint8 of
+    kda_mx4_moe_workspace_size(M, k, inter, E, S, top_k) bytes, no initialisation
+    needed; state_indices None or [M] int32, an index below zero marks a padding
+    row.
+    """
+    lib = load_library()
+    dev = _gpu(x, "x")
+    torch = _torch_module
+    bf = torch.bfloat16
+    for t, name, dims in ((x, "x", 2), (router, "router", 2), (w_up, "w_up", 3), (expert_ids, "expert_ids", 2)):
+        if not isinstance(t, torch.Tensor) or t.dim() != dims:
+            raise ValueError(f"{name} must be a tensor of {dims} dimensions")
+    m, k = rows = x.shape
+    experts, (every, twice, _), top = router.shape[0], w_up.shape, expert_ids.shape[1]
+    inter, shared = twice // 2, every - experts
+    _columns(k, "x")
+    if twice % 64 or shared < 0:
+        raise ValueError(f"w_up must be [E + S, 2 inter, k / 2] with E = {experts} and inter a multiple of 32, "
+                         f"got {tuple(w_up.shape)}")
+    if scoring not in _SCORING:
+        raise ValueError(f"scoring must be sigmoid or softmax, got {scoring!r}")
+    size = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
+    ptrs = (_view(x, "x", bf, rows, dev), _on(router, "router", bf, (experts, k), dev),
+            None if router_bias is None else _on(router_bias, "router_bias", torch.float32, (experts,), dev),
+            *_mx4(w_up, w_up_scales, ("w_up", "w_up_scales"), (every, twice, k), dev),
+            *_mx4(w_down, w_down_scales, ("w_down", "w_down_scales"), (every, k, inter), dev),
+            None if state_indices is None else _on(state_indices, "state_indices", torch.int32, (m,), dev),
+            _view(out, "out", bf, rows, dev), _on(expert_ids, "expert_ids", torch.int32, (m, top), dev),
+            _on(expert_gates, "expert_gates", torch.float32, (m, top), dev),
+            _on(workspace, "workspace", torch.uint8, (size,), dev))
+    _call("kda_mx4_moe", lib.kda_mx4_moe, dev, stream, ptrs,
+          (m, k, inter, experts, shared, top, _row_stride(x, "x"), _row_stride(out, "out"), _SCORING[scoring],
+           1 if renormalise else 0, route_scale, size))
