@@ -95,7 +95,9 @@ kda_status_t kda_mx4_proj(const void* x, const void* x_scales, const void* w, co
   p.N = n;
   int cus = 0;
   if (hipError_t e = kda::device_cus(&cus); e != hipSuccess) return failed(e, "device query");
-  if (hipError_t e = kda::launch_mx4_few(p, cus, static_cast<hipStream_t>(stream)); e != hipSuccess)
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const bool tile = p.xs && num_tokens > 64 && kda::mx4_tile_ok(p);
+  if (hipError_t e = tile ? kda::launch_mx4_tile(p, cus, st) : kda::launch_mx4_few(p, cus, st); e != hipSuccess)
     return failed(e, "4-bit product launch");
   return KDA_OK;
 }
