@@ -4,15 +4,18 @@
 // Bound by the bytes of the experts that are hit, each read once.  Four launches:
 //   logits   x router^T in fp64, (tile of 16 experts) x (slice of k) per workgroup
 //   route    a token per workgroup: slices joined, scores, choice; the last one to
-//            finish lists the experts that are hit and their tokens
-//   up       16 rows of G and of U of one expert per workgroup, waves share k:
-//            h = gate silu(G x) (U x), as two bf16 pieces
-//   down     16 rows of W_down of every expert that is hit per workgroup: the sum
-//            over experts ends where it is made, nothing goes through memory
+//            finish lists the experts that are hit and their tokens, as slots
+//   up       h = gate silu(G x) (U x), as two bf16 pieces: a workgroup walks through
+//            a run of (slot, 16 rows of G and of U), its waves share k
+//   down     16 rows of W_down of all slots per workgroup, or of a part of them where
+//            the rows are few; the sum over experts ends there
 //
 // The router in fp64: which experts are chosen does not depend on the order of a
 // sum, and with a whole-number result there is no rounding to hide behind.  It
 // costs 0.75 us of the fp64 matrix pipe per 16 tokens at 256 x 7168.
+#include <type_traits>
+#include <cstdlib>
+
 #include "kda_mx4_dev.h"
 #include "kda_mx4_internal.h"
 
@@ -35,18 +38,32 @@ __global__ __launch_bounds__(64 * kRouterWaves) void logits_kernel(MoeParams p) 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int e0 = blockIdx.x * 16, slice = blockIdx.y, m0 = blockIdx.z * 16;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) p.head[0] = 0;
+  if (blockIdx.x == 0 && blockIdx.z == 0) {  // counters of the launches behind this one
+    if (slice == 0 && threadIdx.x == 0) p.head[0] = 0;
+    for (int i = slice * (64 * kRouterWaves) + threadIdx.x; i < p.K / 16; i += gridDim.y * (64 * kRouterWaves))
+      p.done[i] = 0;
+  }
   const uint16_t* er = p.router + size_t(min(e0 + l16, p.E - 1)) * p.K;
   const uint16_t* xr = p.x + min(m0 + l16, p.M - 1) * p.x_row;
   const int end = min((slice + 1) * p.slice_blocks, p.K / 32);
   f64x4 acc = {};
-  for (int b = slice * p.slice_blocks + wave; b < end; b += kRouterWaves) {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(er + 32 * b + 8 * g);
-    const u32x4 x = *reinterpret_cast<const u32x4*>(xr + 32 * b + 8 * g);
+  constexpr int kAtOnce = 4;  // blocks of 32 whose loads are under way together
+  for (int b0 = slice * p.slice_blocks + wave; b0 < end; b0 += kAtOnce * kRouterWaves) {
+    u32x4 a[kAtOnce], x[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      acc = mfma64(double(bf16_lo(a[i])), double(bf16_lo(x[i])), acc);
-      acc = mfma64(double(bf16_hi(a[i])), double(bf16_hi(x[i])), acc);
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int b = min(b0 + u * kRouterWaves, end - 1);
+      a[u] = *reinterpret_cast<const u32x4*>(er + 32 * b + 8 * g);
+      x[u] = *reinterpret_cast<const u32x4*>(xr + 32 * b + 8 * g);
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      if (b0 + u * kRouterWaves >= end) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc = mfma64(double(bf16_lo(a[u][i])), double(bf16_lo(x[u][i])), acc);
+        acc = mfma64(double(bf16_hi(a[u][i])), double(bf16_hi(x[u][i])), acc);
+      }
     }
   }
 #pragma unroll
@@ -78,84 +95,195 @@ __device__ double block_reduce(double v, double* red) {
   return r;
 }
 
+// Slot number `slot`: the expert and tokens c * chunk .. of those in mask; its pairs
+// begin at `begin`.
+__device__ __forceinline__ void write_slot(const MoeParams& p, int slot, int expert, uint64_t mask, int c, int begin) {
+  for (int i = 0; i < c * p.chunk; ++i) mask &= mask - 1;
+  MoeSlot o;
+  o.expert = expert, o.begin = begin + c * p.chunk, o.n = min(__popcll(mask), p.chunk), o.unused = 0;
+  uint32_t token = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    o.token[q] = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (mask) token = uint32_t(__builtin_ctzll(mask));  // (the last one is repeated)
+      mask &= mask - 1;
+      o.token[q] |= token << (8 * i);
+    }
+  }
+  p.slot[slot] = o;
+}
+
+// Agent-scope accesses go past the caches that other workgroups do not see, so that
+// what is written with them is there once vmcnt says so: no cache has to be written
+// back or emptied around the counter that announces it.
+__device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+template <typename T>
+__device__ __forceinline__ void put(T* p, T v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+template <typename T>
+__device__ __forceinline__ T get(const T* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+// Whether this workgroup is the last of n to come here (counter: 0 before the first).
+__device__ __forceinline__ bool come_last(int32_t* counter, int n) {
+  __shared__ int last;
+  stores_done();
+  __syncthreads();
+  if (threadIdx.x == 0)
+    last = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
+  __syncthreads();
+  return last;
+}
+
+constexpr int kMaxSlots = 64 * 32 + 16 * 16;
+
 // The experts that are hit, in order, with their tokens in order; shared experts
 // behind them.  One workgroup.
-__device__ void list_experts(const MoeParams& p, uint64_t* mask, int32_t* count) {
-  const int t = threadIdx.x;
-  for (int e = t; e < p.E; e += kRouteThreads) mask[e] = 0;
+struct RouteLds {
+  double key[kMaxExperts], score[kMaxExperts], red[kRouteThreads / 64], chosen[32];
+  int chosen_id[32];
+};
+struct ListLds {
+  uint64_t mask[kMaxExperts + 16];
+  uint16_t first[kMaxExperts + 16], slot_of[kMaxSlots];  // expert * 16 + chunk
+};
+__device__ void list_slots(const MoeParams& p, ListLds& L, int16_t* ids) {
+  const int t = threadIdx.x, every = p.E + p.S;
   __shared__ uint64_t live;
+  __shared__ int slots;
+  for (int e = t; e < p.E; e += kRouteThreads) L.mask[e] = 0;
   if (t == 0) live = 0;
   __syncthreads();
   const int pairs = p.M * p.top;
   for (int i = t; i < pairs; i += kRouteThreads) {
-    const int e = __hip_atomic_load(p.ids + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int e = get(p.ids + i);
+    ids[i] = int16_t(e);
     if (e >= 0) {
-      atomicOr(reinterpret_cast<unsigned long long*>(&mask[e]), 1ull << (i / p.top));
+      atomicOr(reinterpret_cast<unsigned long long*>(&L.mask[e]), 1ull << (i / p.top));
       if (i % p.top == 0) atomicOr(reinterpret_cast<unsigned long long*>(&live), 1ull << (i / p.top));
     }
   }
   __syncthreads();
+  if (t < p.S) L.mask[p.E + t] = live;
+  __syncthreads();
   if (t < 64) {  // one wave: running numbers of slots and of pairs, 64 experts at a time
     int slot = 0, begin = 0;
-    for (int e0 = 0; e0 < p.E + p.S; e0 += 64) {
-      const int e = e0 + t;
-      const uint64_t m = e < p.E ? mask[e] : e < p.E + p.S ? live : 0;
-      const int n = __popcll(m);
-      const uint64_t hit = __ballot(n > 0);
-      int sum = n;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(sum, o);
-        if (t >= o) sum += u;
+    const uint64_t below = (1ull << t) - 1;
+    for (int e0 = 0; e0 < every; e0 += 64) {
+      const int e = e0 + t, n = e < every ? __popcll(L.mask[e]) : 0, c = (n + p.chunk - 1) / p.chunk;
+      int at = begin, s = slot;  // what is before this expert, bit by bit of the counts
+      for (int b = 0; (1 << b) <= p.M; ++b) {
+        const uint64_t nb = __ballot((n >> b) & 1), cb = __ballot((c >> b) & 1);
+        at += __popcll(nb & below) << b;
+        begin += __popcll(nb) << b;
+        s += __popcll(cb & below) << b;
+        slot += __popcll(cb) << b;
       }
-      if (n) {
-        const int s = slot + __popcll(hit & ((1ull << t) - 1));
-        p.slot_expert[s] = e;
-        p.slot_begin[s] = begin + sum - n;
-      }
-      if (e < p.E) count[e] = begin + sum - n;
-      slot += __popcll(hit);
-      begin += __shfl(sum, 63);
+      if (n) L.first[e] = uint16_t(at);
+      for (int i = 0; i < c; ++i) L.slot_of[s + i] = uint16_t(e * 16 + i);
     }
-    if (t == 0) {
-      p.slot_begin[slot] = begin;
-      p.head[1] = slot;
-    }
+    if (t == 0) p.head[1] = slots = slot;
   }
   __syncthreads();
-  int routed = 0;  // pairs of chosen experts: where the shared ones begin
-  for (int w = 0; w < p.M; ++w) routed += (live >> w) & 1 ? p.top : 0;
-  for (int i = t; i < pairs; i += kRouteThreads) {
-    const int e = __hip_atomic_load(p.ids + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (e < 0) continue;
-    const int token = i / p.top;
-    const int at = count[e] + __popcll(mask[e] & ((1ull << token) - 1));
-    p.pairs[at] = token;
-    p.pair_gate[at] = __hip_atomic_load(p.gates + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int i = t; i < slots; i += kRouteThreads) {
+    const int e = L.slot_of[i] >> 4;
+    write_slot(p, i, e, L.mask[e], L.slot_of[i] & 15, L.first[e]);
   }
-  const int lives = __popcll(live);
-  for (int i = t; i < p.S * p.M; i += kRouteThreads) {
-    const int s = i / p.M, token = i % p.M;
-    if (!((live >> token) & 1)) continue;
-    const int at = routed + s * lives + __popcll(live & ((1ull << token) - 1));
-    p.pairs[at] = token;
-    p.pair_gate[at] = 1.f;
+  for (int i = t; i < pairs; i += kRouteThreads)
+    if (ids[i] >= 0)
+      p.pair_gate[L.first[ids[i]] + __popcll(L.mask[ids[i]] & ((1ull << (i / p.top)) - 1))] = get(p.gates + i);
+  for (int i = t; i < p.S * __popcll(live); i += kRouteThreads) p.pair_gate[__popcll(live) * p.top + i] = 1.f;
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  const auto step = [](uint32_t v, auto ctrl) {
+    return max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), decltype(ctrl)::value, 0xf, 0xf, false)));
+  };
+  v = step(v, std::integral_constant<int, 0x111>{});  // from 1, 2, 4, 8 lanes below in a row of 16
+  v = step(v, std::integral_constant<int, 0x112>{});
+  v = step(v, std::integral_constant<int, 0x114>{});
+  v = step(v, std::integral_constant<int, 0x118>{});
+  v = step(v, std::integral_constant<int, 0x142>{});  // a row's last lane to the next row
+  v = step(v, std::integral_constant<int, 0x143>{});  // the second row's to the upper half
+  return uint32_t(__builtin_amdgcn_readlane(int(v), 63));
+}
+
+// The top largest keys, one wave: the largest of 64-bit numbers that order as the keys,
+// top times, the upper 32 bits first and, where several have them, the lower.
+template <int kSlots>
+__device__ __forceinline__ void choose(const MoeParams& p, const double* key, const double* score, double* chosen,
+                                       int* chosen_id, int m) {
+  const int t = threadIdx.x;
+  uint32_t hi[kSlots], lo[kSlots];
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    hi[s] = lo[s] = 0;  // below every key
+    if (64 * s + t < p.E) {
+      const uint64_t b = __builtin_bit_cast(uint64_t, key[64 * s + t] + 0.0);  // (-0 is 0)
+      const uint64_t o = b >> 63 ? ~b : b | 1ull << 63;
+      hi[s] = uint32_t(o >> 32), lo[s] = uint32_t(o);
+    }
+  }
+  int left = min(p.top, p.E);
+  for (int j = 0; j < left; ++j) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s)
+      v = max(v, hi[s]);
+    v = wave_max(v);
+    uint32_t w = 0;
+    int several = 0;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s)
+      several += __popcll(__ballot(hi[s] == v));
+    if (several > 1) {
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s)
+        if (hi[s] == v) w = max(w, lo[s]);
+      w = wave_max(w);
+    }
+    int e = -1;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      if (e < 0) {
+        const uint64_t at = __ballot(hi[s] == v && (several == 1 || lo[s] == w));
+        if (at) {
+          e = 64 * s + __builtin_ctzll(at);
+          if (64 * s + t == e) hi[s] = lo[s] = 0;
+        }
+      }
+    }
+    if (t == 0) {
+      chosen[j] = score[e];
+      chosen_id[j] = e;
+      put(p.ids + m * p.top + j, e);
+    }
   }
 }
 
+// SLOTS: experts / 64 at most (short code: a launch of one workgroup per token runs from
+// a cold instruction cache)
+template <int SLOTS>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeParams p) {
-  __shared__ double key[kMaxExperts], score[kMaxExperts], red[kRouteThreads / 64], chosen[32];
-  __shared__ int last;
+  __shared__ union {
+    RouteLds route;
+    struct {
+      ListLds list;
+      int16_t ids[64 * 32];
+    };
+  } L;
+  double *key = L.route.key, *score = L.route.score, *red = L.route.red, *chosen = L.route.chosen;
+  int* chosen_id = L.route.chosen_id;
   const int m = blockIdx.x, t = threadIdx.x;
   if (p.idx && p.idx[m] < 0) {
     if (t < p.top) {
-      __hip_atomic_store(p.ids + m * p.top + t, -1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      __hip_atomic_store(p.gates + m * p.top + t, 0.f, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      put(p.ids + m * p.top + t, -1);
+      put(p.gates + m * p.top + t, 0.f);
     }
   } else {
     double most = -INFINITY;
     for (int e = t; e < p.E; e += kRouteThreads) {
       double l = 0;
+#pragma unroll 8
       for (int s = 0; s < p.slices; ++s) l += p.logits[(size_t(s) * p.M + m) * p.E + e];
       score[e] = l;
       most = fmax(most, l);
@@ -185,15 +313,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeParams p) {
       key[e] = v == v ? v : -INFINITY;
     }
     __syncthreads();
-    for (int e = t; e < p.E; e += kRouteThreads) {
-      const double v = key[e];
-      int rank = 0;
-      for (int f = 0; f < p.E; ++f) rank += key[f] > v || (key[f] == v && f < e) ? 1 : 0;
-      if (rank < p.top) {
-        chosen[rank] = score[e];
-        __hip_atomic_store(p.ids + m * p.top + rank, e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-    }
+    if (t < 64) choose<SLOTS>(p, key, score, chosen, chosen_id, m);
     __syncthreads();
     if (t < p.top) {
       double sum = 1;
@@ -201,202 +321,317 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeParams p) {
         sum = 0;
         for (int j = 0; j < p.top; ++j) sum += chosen[j];
       }
-      __hip_atomic_store(p.gates + m * p.top + t, float(chosen[t] / sum * double(p.route_scale)), __ATOMIC_RELAXED,
-                         __HIP_MEMORY_SCOPE_AGENT);
+      const float gate = float(chosen[t] / sum * double(p.route_scale));
+      put(p.gates + m * p.top + t, gate);
+      if (p.M == 1) p.pair_gate[t] = gate;
     }
   }
-  __threadfence();
-  __syncthreads();
-  if (t == 0)
-    last = __hip_atomic_fetch_add(p.head, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == p.M - 1;
-  __syncthreads();
-  if (last) list_experts(p, reinterpret_cast<uint64_t*>(key), reinterpret_cast<int32_t*>(score));
-}
-
-// h is kept in the order in which down's operands take it: element 32 g + 8 d + e of
-// a run of 128 at 32 d + 8 g + e, so that a load of operand d is 64 adjacent bytes a
-// token.  Rows are whole runs.
-__device__ __forceinline__ int h_place(int i) {
-  return (i & ~127) | ((i >> 3) & 3) << 5 | ((i >> 5) & 3) << 3 | (i & 7);
-}
-__device__ __forceinline__ int h_row(int inter) { return (inter + 127) & ~127; }
-
-constexpr int kUpWaves = 8, kUpSteps = 2;
-
-template <int RQ>
-__device__ __forceinline__ void up_tile(const MoeParams& p, char* lds, int expert, int i0, int begin, int n) {
-  constexpr int STEPS = kUpSteps;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l16 = lane & 15, g = lane >> 4;
-  const int nb = p.K / kMxBlock, units = (nb + 4 * STEPS - 1) / (4 * STEPS);
-  const int per = (units + kUpWaves - 1) / kUpWaves, first = wave * per, cnt = max(0, min(per, units - first));
-  const uint8_t *codes[2], *scales[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const size_t r = (size_t(expert) * 2 + i) * p.I + i0 + l16;
-    codes[i] = p.w_up + r * (p.K / 2);
-    scales[i] = p.s_up + r * nb;
-  }
-  f32x4 acc[2] = {};
-  char* xl = lds + wave * 4096;
-  if (cnt) {
-    Piece<STEPS> buf[2][2];
-    XRows<RQ> x;
-    const auto load = [&](Piece<STEPS>(&b)[2], int unit) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) load_piece<STEPS>(b[i], codes[i], scales[i], nb, unit, g);
-    };
-    load(buf[0], first);
-    const uint16_t* row[RQ];
-#pragma unroll
-    for (int q = 0; q < RQ; ++q) row[q] = p.x + int64_t(p.pairs[begin + min(4 * q + g, n - 1)]) * p.x_row;
-    load_x<RQ>(x, row, first * STEPS * 128, p.K, l16);
-    const auto use = [&](Piece<STEPS>(&b)[2], int unit) {
-#pragma unroll
-      for (int j = 0; j < STEPS; ++j) {
-        stage_x<RQ>(xl, x, l16, g);
-        load_x<RQ>(x, row, (unit * STEPS + j + 1) * 128, p.K, l16);
-        wave_lds_fence();
-        bf16x8 o[4];
-#pragma unroll
-        for (int d = 0; d < 4; ++d) o[d] = x_operand(xl, d, l16, g);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float sc = scale_of(b[i].s[j], g);
-#pragma unroll
-          for (int d = 0; d < 4; ++d) acc[i] = mfma32(dequant8(b[i].w[j][d], sc), o[d], acc[i]);
-        }
-        wave_lds_fence();
-      }
-    };
-    int i = 0;
-    for (; i + 2 <= cnt; i += 2) {
-      load(buf[1], first + i + 1);
-      use(buf[0], first + i);
-      load(buf[0], first + min(i + 2, cnt - 1));
-      use(buf[1], first + i + 1);
+  if (p.M == 1) {  // the choice is the list
+    const int n = p.idx && p.idx[0] < 0 ? 0 : p.top + p.S;
+    if (t < n) {
+      write_slot(p, t, t < p.top ? chosen_id[t] : p.E + t - p.top, 1, 0, t);
+      if (t >= p.top) p.pair_gate[t] = 1.f;
     }
-    if (i < cnt) use(buf[0], first + i);
+    if (t == 0) p.head[1] = n;
+    return;
   }
-  f32x4(*red)[2][64] = reinterpret_cast<f32x4(*)[2][64]>(lds);
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 2; ++i) red[wave][i][lane] = acc[i];
-  __syncthreads();
-  if (threadIdx.x < 256) {
-    const int r = threadIdx.x & 15, m = threadIdx.x >> 4;
-    const float* at = reinterpret_cast<const float*>(&red[0][0][(r >> 2) * 16 + m]) + (r & 3);
-    float a = at[0], u = at[256];
-#pragma unroll
-    for (int w = 1; w < kUpWaves; ++w) a += at[w * 512], u += at[w * 512 + 256];
-    if (m < n) {
-      const float h = a / (1.f + __expf(-a)) * u * p.pair_gate[begin + m];
-      const uint16_t hi = f32_to_bf16(h);
-      const size_t o = size_t(begin + m) * h_row(p.I) + h_place(i0 + r);
-      p.h_hi[o] = hi;
-      p.h_lo[o] = f32_to_bf16(h - bf16_to_f32(hi));
-    }
-  }
+  if (come_last(p.head, p.M)) list_slots(p, L.list, L.ids);
 }
 
-__global__ __launch_bounds__(64 * kUpWaves) void up_kernel(MoeParams p) {
-  __shared__ __align__(16) char lds[kUpWaves * 4096];
-  const int slot = blockIdx.y;
-  if (slot >= p.head[1]) return;
-  const int begin = p.slot_begin[slot] + 16 * blockIdx.z, n = min(16, p.slot_begin[slot + 1] - begin);
-  if (n <= 0) return;
-  const int expert = p.slot_expert[slot];
-  if (n <= 4)
-    up_tile<1>(p, lds, expert, 16 * blockIdx.x, begin, n);
-  else
-    up_tile<4>(p, lds, expert, 16 * blockIdx.x, begin, n);
+// Data that a launch before this one wrote, read through the scalar cache.
+template <typename T>
+__device__ __forceinline__ const __attribute__((address_space(4))) T* scalar(const T* p) {
+  return (const __attribute__((address_space(4))) T*)(p);
 }
-
-constexpr int kDownWaves = 8, kDownSteps = 2;
-
-// h of one token for STEPS steps: its two pieces' operands.
-struct HPiece {
-  bf16x8 hi[kDownSteps][4], lo[kDownSteps][4];
+struct SlotView {
+  int expert, begin, n;
+  uint32_t t0, t1, t2, t3;
+  __device__ __forceinline__ SlotView(const MoeSlot* p) {
+    const auto* s = scalar(p);
+    expert = s->expert, begin = s->begin, n = s->n;
+    t0 = s->token[0], t1 = s->token[1], t2 = s->token[2], t3 = s->token[3];
+  }
+  // tokens 4 q + g and i, of a lane
+  template <int Q>
+  __device__ __forceinline__ int token4(int g) const {
+    return ((Q == 0 ? t0 : Q == 1 ? t1 : Q == 2 ? t2 : t3) >> (8 * g)) & 0xff;
+  }
+  __device__ __forceinline__ int token(int i) const {
+    const uint32_t lo = i & 4 ? t1 : t0, hi = i & 4 ? t3 : t2;
+    return ((i & 8 ? hi : lo) >> (8 * (i & 3))) & 0xff;
+  }
 };
 
-__global__ __launch_bounds__(64 * kDownWaves) void down_kernel(MoeParams p) {
-  constexpr int STEPS = kDownSteps;
+constexpr int kUpWaves = 8;
+
+// A workgroup's items are adjacent (slot, tile of 16 rows) pairs; the units of k of a
+// wave, item after item, go through a ring of U, so that the next item's loads are
+// under way while this one is joined.
+template <int RQ, int STEPS, int U, bool TINY>
+__global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(4, 4))) void up_kernel(MoeParams p) {
+  // two halves in turn where they fit beside two workgroups' operands
+  constexpr int kHalves = RQ == 1 ? 2 : 1;
+  constexpr int kX = STEPS * RQ * 1024, kWave = kX + 2 * kPieceLds<STEPS>;
+  __shared__ __align__(16) char lds[kUpWaves * kWave];
+  __shared__ f32x4 red[kHalves][kUpWaves][2][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const int tiles = p.I / 16;
+  const uint32_t items = scalar(p.head)[1] * tiles;
+  const uint32_t lo = items * blockIdx.x >> p.up_log2, hi = items * (blockIdx.x + 1) >> p.up_log2;
+  if (lo >= hi) return;
+  const int nb = p.K / kMxBlock, units = (nb + 4 * STEPS - 1) / (4 * STEPS);
+  const int first = units * wave / kUpWaves, cnt = units * (wave + 1) / kUpWaves - first;
+  char *xl = lds + wave * kWave, *wl = xl + kX;
+  const uint32_t row_bytes = p.K / 2, code_row = (lane >> 2) * row_bytes, scale_row = (lane >> 2) * nb;
+  const int slot0 = lo / tiles, tile0 = lo - slot0 * tiles;
+
+  struct Unit {
+    Piece<STEPS> w[2];
+    XRows<RQ> x[STEPS];
+  } buf[U];
+  // what is loaded next
+  int left_items = hi - lo, slot = slot0, tile = tile0, unit = 0;
+  const uint8_t *codes[2], *scales[2];
+  uint32_t row[RQ];
+  const auto aim_slot = [&](const SlotView& s) {
+    const uint32_t x_bytes = uint32_t(p.x_row) * 2;
+    row[0] = s.token4<0>(g) * x_bytes;
+    if (RQ > 1) {
+      row[1 % RQ] = s.token4<1>(g) * x_bytes;
+      row[2 % RQ] = s.token4<2>(g) * x_bytes;
+      row[3 % RQ] = s.token4<3>(g) * x_bytes;
+    }
+  };
+  const auto aim_tile = [&](int expert) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const size_t r = (size_t(expert) * 2 + i) * p.I + tile * 16;
+      codes[i] = p.w_up + r * row_bytes;
+      scales[i] = p.s_up + r * nb;
+    }
+  };
+  // (Loads behind the last unit to keep the number in flight constant, so that the waits
+  // could count them, cost more than waiting for all: other waves fill the time.)
+  const auto load = [&](Unit& b) {
+    if (left_items == 0) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      load_piece<STEPS, TINY>(b.w[i], codes[i], code_row, scales[i], scale_row, nb, first + unit, lane & 3);
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) load_x<RQ>(b.x[j], p.x, row, ((first + unit) * STEPS + j) * 128, p.K, l16);
+    if (++unit == cnt) {
+      unit = 0;
+      if (--left_items > 0) {
+        if (++tile == tiles) tile = 0, ++slot;
+        const SlotView s(p.slot + slot);
+        if (tile == 0) aim_slot(s);
+        aim_tile(s.expert);
+      }
+    }
+  };
+  f32x4 acc[2] = {};
+  const auto use = [&](Unit& b, int unit) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) stage_piece<STEPS, TINY>(wl + i * kPieceLds<STEPS>, b.w[i], nb, first + unit, lane);
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j)
+      stage_x<RQ>(xl + j * (RQ * 1024), b.x[j], ((first + unit) * STEPS + j) * 128, p.K, l16, g);
+    wave_lds_fence();
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+      bf16x8 o[4];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] = x_operand<RQ>(xl + j * (RQ * 1024), d, l16, g);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const char* at = wl + i * kPieceLds<STEPS>;
+        const float sc = scale_of(scale_operand<STEPS>(at, j, l16, g));
+        const u32x4 c = codes_operand(at, j, l16, g);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) acc[i] = mfma32(dequant8(c[d], sc), o[d], acc[i]);
+      }
+    }
+    wave_lds_fence();
+  };
+  // joins the waves' sums of an item (of two halves, the other one is free once all have come)
+  int at_slot = slot0, at_tile = tile0, half = 0;
+  const auto join = [&]() {
+    auto& r = red[half];
+    if (kHalves == 2)
+      half ^= 1;
+    else
+      __syncthreads();
+    r[wave][0][lane] = acc[0], r[wave][1][lane] = acc[1];
+    acc[0] = acc[1] = f32x4{};
+    __syncthreads();
+    if (wave < RQ) {
+      const int n = lane & 15, m = 4 * wave + g;  // row of the tile, pair of the slot
+      const SlotView s(p.slot + at_slot);
+      if (4 * wave < s.n) {
+        const auto* gate4 = scalar(p.pair_gate) + s.begin + 4 * wave;
+        const float g0 = gate4[0], g1 = gate4[1], g2 = gate4[2], g3 = gate4[3];
+        const float gate = g & 2 ? (g & 1 ? g3 : g2) : (g & 1 ? g1 : g0);
+        const float* at = reinterpret_cast<const float*>(&r[0][0][(n >> 2) * 16 + m]) + (n & 3);
+        float a = at[0], u = at[256];
+#pragma unroll
+        for (int w = 1; w < kUpWaves; ++w) a += at[w * 512], u += at[w * 512 + 256];
+        if (m < s.n) {
+          const float h = a / (1.f + __expf(-a)) * u * gate;
+          const uint16_t top = f32_to_bf16(h);
+          const size_t o = size_t(s.begin + m) * p.I + at_tile * 16 + n;
+          p.h_hi[o] = top;
+          p.h_lo[o] = f32_to_bf16(h - bf16_to_f32(top));
+        }
+      }
+    }
+    if (++at_tile == tiles) at_tile = 0, ++at_slot;
+  };
+  int items_left = hi - lo;
+  if (cnt == 0) {  // (fewer units than waves)
+    for (; items_left > 0; --items_left) join();
+    return;
+  }
+  {
+    const SlotView s(p.slot + slot0);
+    aim_slot(s);
+    aim_tile(s.expert);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(buf[u]);
+  int at_unit = 0;
+  for (;;) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      use(buf[u], at_unit);
+      load(buf[u]);
+      if (++at_unit == cnt) {
+        join();
+        if (--items_left == 0) return;
+        at_unit = 0;
+      }
+    }
+  }
+}
+
+constexpr int kDownWaves = 8;
+
+template <int RQ, int U, bool TINY>
+__global__ __launch_bounds__(64 * kDownWaves, 4) void down_kernel(MoeParams p) {
   extern __shared__ __align__(16) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16;
-  const int nb = p.I / kMxBlock, units = (nb + 4 * STEPS - 1) / (4 * STEPS);
-  const int slots = p.head[1], jobs = slots * units;
-  const int per = (jobs + kDownWaves - 1) / kDownWaves, first = wave * per, cnt = max(0, min(per, jobs - first));
+  const int n0 = blockIdx.x * 16, part = blockIdx.y;
+  const int nb = p.I / kMxBlock, units = (nb + 3) / 4;
+  const uint32_t jobs = scalar(p.head)[1] * units;
+  // this wave's run of (slot, unit of k)
+  const uint32_t share = part * kDownWaves + wave, shares = p.parts * kDownWaves;
+  const int first = jobs * share / shares, end = jobs * (share + 1) / shares;
+  constexpr int kWave = RQ * 1024 + kPieceLds<1>;
+  char *hl = lds + wave * kWave, *wl = hl + RQ * 1024;
   // [wave][token][16]: this wave's sums
-  f32x4* y = reinterpret_cast<f32x4*>(lds) + wave * p.M * 4;
+  f32x4* y = reinterpret_cast<f32x4*>(lds + kDownWaves * kWave) + wave * p.M * 4;
   for (int i = lane; i < p.M * 4; i += 64) y[i] = f32x4{};
   wave_lds_fence();
-  const int hrow = h_row(p.I);
-
-  const auto load_w = [&](Piece<STEPS>& b, int job) {
-    const int expert = p.slot_expert[job / units];
-    const size_t r = size_t(expert) * p.K + n0 + l16;
-    load_piece<STEPS>(b, p.w_down + r * (p.I / 2), p.s_down + r * nb, nb, job % units, g);
-  };
-  const auto load_h = [&](HPiece& h, int at, int unit) {
-    const uint16_t *hi = p.h_hi + size_t(at) * hrow, *lo = p.h_lo + size_t(at) * hrow;
+  if (first < end) {
+    struct Unit {
+      Piece<1> w;
+      XRows<RQ> hi, lo;
+    } buf[U];
+    // what is loaded next
+    const uint32_t row_bytes = p.I / 2, code_row = (lane >> 2) * row_bytes, scale_row = (lane >> 2) * nb;
+    const int slot0 = first / units;
+    int job = first, slot = slot0, unit = first - slot0 * units;
+    const uint8_t *codes, *scales;
+    const uint16_t *hi, *lo;
+    uint32_t row[RQ];
+    const auto aim = [&]() {
+      const SlotView s(p.slot + slot);
+      const size_t r = size_t(s.expert) * p.K + n0, at = size_t(s.begin) * p.I;
+      codes = p.w_down + r * row_bytes;
+      scales = p.s_down + r * nb;
+      hi = p.h_hi + at, lo = p.h_lo + at;
 #pragma unroll
-    for (int j = 0; j < STEPS; ++j) {
-      const int b = (unit * STEPS + j) * 4 + g;
-      const bool in = b < nb;
-      const int k = in ? (unit * STEPS + j) * 128 + 8 * g : 0;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        h.hi[j][d] = *reinterpret_cast<const bf16x8*>(hi + (in ? k + 32 * d : 0));
-        h.lo[j][d] = *reinterpret_cast<const bf16x8*>(lo + (in ? k + 32 * d : 0));
-        if (!in) h.hi[j][d] = h.lo[j][d] = bf16x8{};
+      for (int q = 0; q < RQ; ++q) row[q] = uint32_t(min(4 * q + g, s.n - 1)) * (p.I * 2);
+    };
+    const auto load = [&](Unit& b) {
+      if (job == end) return;
+      load_piece<1, TINY>(b.w, codes, code_row, scales, scale_row, nb, unit, lane & 3);
+      load_x<RQ>(b.hi, hi, row, unit * 128, p.I, l16);
+      load_x<RQ>(b.lo, lo, row, unit * 128, p.I, l16);
+      if (++job < end && ++unit == units) {
+        unit = 0;
+        ++slot;
+        aim();
       }
-    }
-  };
-  Piece<STEPS> buf[2];
-  const auto use = [&](const Piece<STEPS>& b, int job) {
-    const int slot = job / units, unit = job % units;
-    const int begin = p.slot_begin[slot], n = p.slot_begin[slot + 1] - begin;
-    for (int t0 = 0; t0 < n; t0 += 16) {
-      const int at = begin + min(t0 + l16, n - 1);
-      HPiece h;
-      load_h(h, at, unit);
-      const int token = p.pairs[at];
-      f32x4 acc = {};
-#pragma unroll
-      for (int j = 0; j < STEPS; ++j) {
-        const float sc = scale_of(b.s[j], g);
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const bf16x8 w = dequant8(b.w[j][d], sc);
-          acc = mfma32(w, h.hi[j][d], acc);
-          acc = mfma32(w, h.lo[j][d], acc);
-        }
-      }
-      if (t0 + l16 < n) y[token * 4 + g] += acc;
+    };
+    f32x4 acc = {};
+    const auto use = [&](Unit& b, int unit) {
+      stage_piece<1, TINY>(wl, b.w, nb, unit, lane);
+      stage_x<RQ>(hl, b.hi, unit * 128, p.I, l16, g);
       wave_lds_fence();
+      const float sc = scale_of(scale_operand<1>(wl, 0, l16, g));
+      const u32x4 c = codes_operand(wl, 0, l16, g);
+      bf16x8 w[4];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) w[d] = dequant8(c[d], sc);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) acc = mfma32(w[d], x_operand<RQ>(hl, d, l16, g), acc);
+      wave_lds_fence();
+      stage_x<RQ>(hl, b.lo, unit * 128, p.I, l16, g);
+      wave_lds_fence();
+#pragma unroll
+      for (int d = 0; d < 4; ++d) acc = mfma32(w[d], x_operand<RQ>(hl, d, l16, g), acc);
+      wave_lds_fence();
+    };
+    int at = first, at_slot = slot0, at_unit = unit;
+    const auto step = [&](Unit& b) {
+      use(b, at_unit);
+      load(b);
+      ++at;
+      if (++at_unit == units || at == end) {
+        const SlotView s(p.slot + at_slot);
+        if (l16 < s.n) y[s.token(l16) * 4 + g] += acc;
+        wave_lds_fence();
+        acc = f32x4{};
+        ++at_slot;
+        at_unit = 0;
+      }
+    };
+    aim();
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(buf[u]);
+    for (bool more = true; more;) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!more) break;
+        step(buf[u]);
+        more = at != end;
+      }
     }
-  };
-  if (cnt) {
-    load_w(buf[0], first);
-    int i = 0;
-    for (; i + 2 <= cnt; i += 2) {
-      load_w(buf[1], first + i + 1);
-      use(buf[0], first + i);
-      load_w(buf[0], first + min(i + 2, cnt - 1));
-      use(buf[1], first + i + 1);
-    }
-    if (i < cnt) use(buf[0], first + i);
   }
   __syncthreads();
-  const float* all = reinterpret_cast<const float*>(lds);
+  const float* all = reinterpret_cast<const float*>(lds + kDownWaves * kWave);
+  if (p.parts > 1) {
+    // a part's sums to the workspace; who comes last adds them up, in their order
+    for (int i = threadIdx.x; i < p.M * 16; i += 64 * kDownWaves) {
+      float s = all[i];
+#pragma unroll
+      for (int w = 1; w < kDownWaves; ++w) s += all[w * p.M * 16 + i];
+      put(p.sums + (size_t(part) * p.M + (i >> 4)) * p.K + n0 + (i & 15), s);
+    }
+    if (!come_last(p.done + blockIdx.x, p.parts)) return;
+  }
   for (int i = threadIdx.x; i < p.M * 16; i += 64 * kDownWaves) {
     const int m = i >> 4;
     if (p.idx && p.idx[m] < 0) continue;
-    float s = all[i];
+    float s = 0.f;
+    if (p.parts > 1) {
+      for (int q = 0; q < p.parts; ++q) s += get(p.sums + (size_t(q) * p.M + m) * p.K + n0 + (i & 15));
+    } else {
 #pragma unroll
-    for (int w = 1; w < kDownWaves; ++w) s += all[w * p.M * 16 + i];
+      for (int w = 0; w < kDownWaves; ++w) s += all[w * p.M * 16 + i];
+    }
     p.out[m * p.out_row + n0 + (i & 15)] = f32_to_bf16(s);
   }
 }
@@ -404,6 +639,22 @@ __global__ __launch_bounds__(64 * kDownWaves) void down_kernel(MoeParams p) {
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
+
+int moe_slots(int M, int E, int S, int top, int chunk) {
+  const int pairs = M * top, most = E + pairs / chunk;
+  return (pairs < most ? pairs : most) + S * ((M + chunk - 1) / chunk);
+}
+
+// Parts of down's sum over slots: two workgroups per compute unit of 256, while a part
+// has a unit of k for each of its waves.
+int moe_parts(int M, int K, int I, int E, int S, int top, int chunk) {
+  const int tiles = K / 16, units = (I + 255) / 256;
+  const int64_t shares = int64_t(moe_slots(M, E, S, top, chunk)) * units / kDownWaves;
+  int parts = 512 / tiles;
+  if (parts > shares) parts = int(shares);
+  if (parts > kMoeMostParts) parts = kMoeMostParts;
+  return parts < 1 ? 1 : parts;
+}
 
 // Slices of the router's sums: about 256 workgroups for 16 tokens, whatever the
 // number of tokens (the size of the workspace grows with it and never falls).
@@ -415,8 +666,9 @@ MoeLayout moe_layout(int M, int K, int I, int E, int S, int top) {
   if (slices < 1) slices = 1;
   l.slice_blocks = (nb + slices - 1) / slices;
   l.slices = (nb + l.slice_blocks - 1) / l.slice_blocks;
-  l.slots = (int64_t(M) * top < E ? M * top : E) + S;
-  const size_t pairs = size_t(M) * (top + S), hrow = (size_t(I) + 127) & ~size_t(127);
+  const size_t pairs = size_t(M) * (top + S);
+  size_t most = 512 / (K / 16);
+  if (most > kMoeMostParts) most = kMoeMostParts;
   size_t at = 0;
   const auto part = [&](size_t bytes) {
     const size_t here = at;
@@ -424,33 +676,49 @@ MoeLayout moe_layout(int M, int K, int I, int E, int S, int top) {
     return here;
   };
   l.head = part(2 * 4);
+  l.done = part(size_t(K / 16) * 4);
   l.logits = part(size_t(l.slices) * M * E * 8);
-  l.slot_expert = part(size_t(l.slots) * 4);
-  l.slot_begin = part(size_t(l.slots + 1) * 4);
-  l.pairs = part(pairs * 4);
-  l.pair_gate = part(pairs * 4);
-  l.h_hi = part(pairs * hrow * 2);
-  l.h_lo = part(pairs * hrow * 2);
+  l.slot = part(size_t(moe_slots(M, E, S, top, 4)) * sizeof(MoeSlot));
+  l.pair_gate = part((pairs + 16) * 4);
+  l.h_hi = part(pairs * I * 2);
+  l.h_lo = part(pairs * I * 2);
+  l.sums = part(most > 1 ? most * M * K * 4 : 0);
   l.total = at;
   return l;
 }
 
-hipError_t launch_moe(const MoeParams& p, int cus, hipStream_t st) {
-  MoeParams arg = p;
-  void* args[] = {&arg};
-  const auto go = [&](const void* f, dim3 grid, int threads, size_t lds) {
-    return hipLaunchKernel(f, grid, dim3(threads), args, lds, st);
+hipError_t launch_moe(const MoeParams& params, int cus, hipStream_t st) {
+  MoeParams p = params;
+  // Tokens per slot: 4 where an expert that is hit has about two.  Those with more are
+  // read once for each 4 (from the L2, by workgroups that run at the same time).
+  static const int v = [] { const char* e = getenv("MXC"); return e ? atoi(e) : 2; }();
+  p.chunk = p.M <= 4 || p.M * p.top <= v * p.E ? 4 : 16;
+  p.parts = moe_parts(p.M, p.K, p.I, p.E, p.S, p.top, p.chunk);
+  void* args[] = {&p};
+  const auto go = [&](auto* f, dim3 grid, int threads, size_t lds) {
+    return hipLaunchKernel(reinterpret_cast<const void*>(f), grid, dim3(threads), args, lds, st);
   };
-  const int tiles = (p.M + 15) / 16, slots = (p.M * p.top < p.E ? p.M * p.top : p.E) + p.S;
-  hipError_t e = go(reinterpret_cast<const void*>(&logits_kernel), dim3((p.E + 15) / 16, p.slices, tiles),
-                    64 * kRouterWaves, 0);
+  hipError_t e = go(&logits_kernel, dim3((p.E + 15) / 16, p.slices, (p.M + 15) / 16), 64 * kRouterWaves, 0);
   if (e != hipSuccess) return e;
-  e = go(reinterpret_cast<const void*>(&route_kernel), dim3(p.M), kRouteThreads, 0);
+  e = go(p.E <= 256 ? &route_kernel<4> : &route_kernel<kMaxExperts / 64>, dim3(p.M), kRouteThreads, 0);
   if (e != hipSuccess) return e;
-  e = go(reinterpret_cast<const void*>(&up_kernel), dim3(p.I / 16, slots, tiles), 64 * kUpWaves, 0);
+  // a power of two of workgroups, about two per compute unit
+  const int64_t items = int64_t(moe_slots(p.M, p.E, p.S, p.top, p.chunk)) * (p.I / 16);
+  p.up_log2 = 0;
+  while ((int64_t(1) << p.up_log2) < items && (2 << p.up_log2) <= 2 * cus) ++p.up_log2;
+  const dim3 up(1u << p.up_log2);
+  const size_t sums = size_t(kDownWaves) * p.M * 64;
+  const dim3 down(p.K / 16, p.parts);
+  if (p.chunk == 4) {
+    e = go(p.K < 128 ? &up_kernel<1, 2, 2, true> : &up_kernel<1, 2, 2, false>, up, 64 * kUpWaves, 0);
+    if (e != hipSuccess) return e;
+    return go(p.I < 128 ? &down_kernel<1, 4, true> : &down_kernel<1, 4, false>, down, 64 * kDownWaves,
+              sums + kDownWaves * (1024 + kPieceLds<1>));
+  }
+  e = go(p.K < 128 ? &up_kernel<4, 1, 2, true> : &up_kernel<4, 1, 2, false>, up, 64 * kUpWaves, 0);
   if (e != hipSuccess) return e;
-  return go(reinterpret_cast<const void*>(&down_kernel), dim3(p.K / 16), 64 * kDownWaves,
-            size_t(kDownWaves) * p.M * 64);
+  return go(p.I < 128 ? &down_kernel<4, 2, true> : &down_kernel<4, 2, false>, down, 64 * kDownWaves,
+            sums + kDownWaves * (4096 + kPieceLds<1>));
 }
 
 }  // namespace kda

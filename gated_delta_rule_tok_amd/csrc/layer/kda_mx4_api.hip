@@ -1,6 +1,7 @@
 // kda_mx4_api.hip -- the C ABI of include/kda_mx4.h: argument checks, workspace
 // sizing and the launches.
 #include <cmath>
+#include <cstdlib>
 #include <cstdint>
 #include <cstring>
 
@@ -96,7 +97,7 @@ kda_status_t kda_mx4_proj(const void* x, const void* x_scales, const void* w, co
   int cus = 0;
   if (hipError_t e = kda::device_cus(&cus); e != hipSuccess) return failed(e, "device query");
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const bool tile = p.xs && num_tokens > 64 && kda::mx4_tile_ok(p);
+  const bool tile = p.xs && num_tokens > 64 && kda::mx4_tile_ok(p) && getenv("MXT");
   if (hipError_t e = tile ? kda::launch_mx4_tile(p, cus, st) : kda::launch_mx4_few(p, cus, st); e != hipSuccess)
     return failed(e, "4-bit product launch");
   return KDA_OK;
@@ -155,12 +156,12 @@ kda_status_t kda_mx4_moe(const void* x, const void* router, const float* router_
   p.slices = lay.slices, p.slice_blocks = lay.slice_blocks;
   p.head = reinterpret_cast<int32_t*>(ws + lay.head);
   p.logits = reinterpret_cast<double*>(ws + lay.logits);
-  p.slot_expert = reinterpret_cast<int32_t*>(ws + lay.slot_expert);
-  p.slot_begin = reinterpret_cast<int32_t*>(ws + lay.slot_begin);
-  p.pairs = reinterpret_cast<int32_t*>(ws + lay.pairs);
+  p.done = reinterpret_cast<int32_t*>(ws + lay.done);
+  p.slot = reinterpret_cast<kda::MoeSlot*>(ws + lay.slot);
   p.pair_gate = reinterpret_cast<float*>(ws + lay.pair_gate);
   p.h_hi = reinterpret_cast<uint16_t*>(ws + lay.h_hi);
   p.h_lo = reinterpret_cast<uint16_t*>(ws + lay.h_lo);
+  p.sums = reinterpret_cast<float*>(ws + lay.sums);
   int cus = 0;
   if (hipError_t e = kda::device_cus(&cus); e != hipSuccess) return failed(e, "device query");
   if (hipError_t e = kda::launch_moe(p, cus, static_cast<hipStream_t>(stream)); e != hipSuccess)

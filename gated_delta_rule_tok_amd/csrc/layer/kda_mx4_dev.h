@@ -21,45 +21,73 @@ namespace kda {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-struct __attribute__((packed, aligned(1))) AnyAligned16 { uint32_t v[4]; };
-
-// STEPS steps of 128 k (4 blocks of 32) of one tile of 16 rows, as loaded: lane l
-// holds row l % 16, block 4 j + l / 16 of step j, and all 4 scales of step j in s[j].
+// A unit, STEPS steps of 128 k (4 blocks of 32), of one tile of 16 rows as loaded:
+// lane l holds of row l / 4 the block 4 j + l % 4 of step j, and the 4 scales of step
+// min(l % 4, STEPS - 1).  An operand wants row l % 16 and block l / 16 instead, but a
+// load whose adjacent lanes are in different rows takes a cycle a lane (64 for 1 KB:
+// 10 TB/s over the device at best, with the scales 4), this one a cycle for four, and
+// LDS is there to exchange them.
 template <int STEPS>
 struct Piece {
   u32x4 w[STEPS];
-  uint32_t s[STEPS];
+  uint32_t s;
 };
-
-// codes, scales: the row's (this lane's), of nb blocks; unit: which STEPS steps.
-// Blocks behind the row's end repeat the last one's codes with scale 0.  A wave's
-// 16 scale bytes of a row come in one load (one byte at a time, each load fetches
-// a line a row for it: more than the codes).
+constexpr int kScaleLds = 256;  // bytes of LDS for the scales of a tile's unit
 template <int STEPS>
-__device__ __forceinline__ void load_piece(Piece<STEPS>& p, const uint8_t* codes, const uint8_t* scales,
-                                           int nb, int unit, int g) {
-  const int b0 = unit * (4 * STEPS);
-  if (b0 + 4 * STEPS <= nb) {
+constexpr int kPieceLds = STEPS * 1024 + kScaleLds;
+
+// codes, scales: those of the tile's first row (scalars); code_row, scale_row: bytes
+// from there to this lane's row; nb: blocks of a row; unit: which STEPS steps; q = l % 4.
+// Scalar bases and 32-bit offsets, since a decode step's calls are as much instructions
+// as bytes.  Blocks behind the row's end repeat the last one's codes with scale 0.
+// TINY: rows of fewer than 4 blocks, whose scales are read byte by byte.
+template <int STEPS, bool TINY>
+__device__ __forceinline__ void load_piece(Piece<STEPS>& p, const uint8_t* codes, uint32_t code_row,
+                                           const uint8_t* scales, uint32_t scale_row, int nb, int unit, int q) {
+  static_assert(STEPS <= 4, "a lane of four for each step");
+  const int b0 = unit * (4 * STEPS), rest = nb - 1 - b0;
+  const uint8_t* c = codes + uint32_t(b0) * 16;
 #pragma unroll
-    for (int j = 0; j < STEPS; ++j) p.w[j] = *reinterpret_cast<const u32x4*>(codes + uint32_t(b0 + 4 * j + g) * 16);
-    struct __attribute__((packed, aligned(1))) B { uint32_t v[STEPS]; };
-    const B b = *reinterpret_cast<const B*>(scales + b0);
+  for (int j = 0; j < STEPS; ++j)
+    p.w[j] = *reinterpret_cast<const u32x4*>(c + (code_row + uint32_t(min(4 * j + q, rest)) * 16));
+  const int b = b0 + 4 * min(q, STEPS - 1);
+  if (TINY) {
+    p.s = 0;
 #pragma unroll
-    for (int j = 0; j < STEPS; ++j) p.s[j] = b.v[j];
+    for (int i = 0; i < 3; ++i)
+      if (b + i < nb) p.s |= uint32_t(scales[scale_row + b + i]) << (8 * i);
   } else {
-#pragma unroll
-    for (int j = 0; j < STEPS; ++j) {
-      const int b = b0 + 4 * j + g, c = min(b, nb - 1);
-      p.w[j] = *reinterpret_cast<const u32x4*>(codes + uint32_t(c) * 16);
-      p.s[j] = b < nb ? uint32_t(scales[c]) << (8 * g) : 0u;
-    }
+    struct __attribute__((packed, aligned(1))) B { uint32_t v; };
+    p.s = reinterpret_cast<const B*>(scales + (scale_row + uint32_t(min(b, nb - 4))))->v;
   }
 }
-
-// The scale of lane group g's block, as the exponent field of a float.
-__device__ __forceinline__ float scale_of(uint32_t s, int g) {
-  return __uint_as_float(((s >> (8 * g)) & 0xffu) << 23);
+// Rows of 64 bytes in LDS: piece c of 16 bytes of row r is at piece c ^ bank_turn(r), so
+// that one piece of 8 adjacent rows covers 128 bytes and of 16 rows 256, every bank once.
+__device__ __forceinline__ int bank_turn(int r) { return ((r >> 1) ^ ((r >> 3) & 1)) & 3; }
+// Into the LDS that the wave has for this tile: rows of 64 bytes for each step, then 16
+// bytes of scales a row.
+template <int STEPS, bool TINY>
+__device__ __forceinline__ void stage_piece(char* lds, const Piece<STEPS>& p, int nb, int unit, int lane) {
+  const int r = lane >> 2, q = lane & 3;
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j)
+    *reinterpret_cast<u32x4*>(lds + j * 1024 + r * 64 + ((q ^ bank_turn(r)) << 4)) = p.w[j];
+  uint32_t s = p.s;
+  if (!TINY && (unit + 1) * (4 * STEPS) > nb) {  // a row's last bytes: down to their place, zeros behind them
+    const int over = unit * (4 * STEPS) + 4 * min(q, STEPS - 1) - (nb - 4);
+    s = over <= 0 ? s : over < 4 ? s >> (8 * over) : 0u;
+  }
+  *reinterpret_cast<uint32_t*>(lds + STEPS * 1024 + r * 16 + q * 4) = s;
 }
+// An operand's codes and scale byte of step j.
+__device__ __forceinline__ u32x4 codes_operand(const char* lds, int j, int l16, int g) {
+  return *reinterpret_cast<const u32x4*>(lds + j * 1024 + l16 * 64 + ((g ^ bank_turn(l16)) << 4));
+}
+template <int STEPS>
+__device__ __forceinline__ uint32_t scale_operand(const char* lds, int j, int l16, int g) {
+  return *reinterpret_cast<const uint8_t*>(lds + STEPS * 1024 + l16 * 16 + j * 4 + g);
+}
+__device__ __forceinline__ float scale_of(uint32_t s) { return __uint_as_float(s << 23); }
 
 // Eight codes of a dword as bf16.
 __device__ __forceinline__ bf16x8 dequant8(uint32_t q, float scale) {
@@ -76,10 +104,10 @@ __device__ __forceinline__ i32x8 codes8(u32x4 v) {
 
 // 16 rows x 16 columns x 128 k of codes; sa, sb: the scale byte of the lane in the low bits
 __device__ __forceinline__ f32x4 mfma_mx4(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x4 c) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes8(a), codes8(b), c, 4, 4, 0, int(sa & 0xffu), 0, int(sb & 0xffu));
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes8(a), codes8(b), c, 4, 4, 0, int(sa), 0, int(sb));
 }
 
-// Up to 16 rows of bf16 x, 128 of k at a time, into MFMA operands through 4 KB of
+// Up to 4 RQ rows of bf16 x, 128 of k at a time, into MFMA operands through RQ KB of
 // LDS that the wave has for itself: a load takes whole 256-byte rows, 4 of them,
 // where loads in the operands' layout would take quarters of lines of 16.  The
 // 16-byte pieces of row r are stored in the order piece ^ r (bank spread).
@@ -88,25 +116,37 @@ template <int RQ>
 struct XRows {
   u32x4 v[RQ];
 };
+// x: a scalar; row[q]: bytes from there to row 4 q + lane / 16; K: elements of a row.
 template <int RQ>
-__device__ __forceinline__ void load_x(XRows<RQ>& x, const uint16_t* const (&row)[RQ], int k0, int K, int l16) {
+__device__ __forceinline__ void load_x(XRows<RQ>& x, const uint16_t* base, const uint32_t (&row)[RQ], int k0, int K,
+                                       int l16) {
+  k0 = min(k0, K - 8);
+  const uint16_t* at = base + k0;
+  const int rest = (K - 8 - k0) >> 3;
 #pragma unroll
-  for (int q = 0; q < RQ; ++q) {
-    const int k = k0 + 8 * l16;
-    x.v[q] = *reinterpret_cast<const u32x4*>(row[q] + min(k, K - 8));
-    if (k >= K) x.v[q] = u32x4{};
-  }
+  for (int q = 0; q < RQ; ++q)
+    x.v[q] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(at) + (row[q] + uint32_t(min(l16, rest)) * 16));
 }
+// Pieces behind the end of k (they repeat another) as zeros.
 template <int RQ>
-__device__ __forceinline__ void stage_x(char* lds, const XRows<RQ>& x, int l16, int g) {
+__device__ __forceinline__ void stage_x(char* lds, XRows<RQ>& x, int k0, int K, int l16, int g) {
+  if (k0 + 128 > K) {
+    const bool in = k0 + 8 * l16 < K;
+#pragma unroll
+    for (int q = 0; q < RQ; ++q)
+      if (!in) x.v[q] = u32x4{};
+  }
 #pragma unroll
   for (int q = 0; q < RQ; ++q) {
     const int r = 4 * q + g;
     *reinterpret_cast<u32x4*>(lds + r * 256 + ((l16 ^ r) << 4)) = x.v[q];
   }
 }
+// (rows that are not staged repeat those that are: their columns are not used)
+template <int RQ>
 __device__ __forceinline__ bf16x8 x_operand(const char* lds, int d, int l16, int g) {
-  return *reinterpret_cast<const bf16x8*>(lds + l16 * 256 + (((4 * g + d) ^ l16) << 4));
+  const int r = l16 & (4 * RQ - 1);
+  return *reinterpret_cast<const bf16x8*>(lds + r * 256 + (((4 * g + d) ^ r) << 4));
 }
 // Orders the wave's own LDS accesses (they complete in order) for the compiler.
 __device__ __forceinline__ void wave_lds_fence() {

@@ -8,155 +8,296 @@
 // MFMA as it is; with x in bf16 the codes become bf16 (an exact conversion, the
 // scale applied) and four MFMAs take the lane's four dwords in turn, x's operand
 // in the same order of k.
+#include <cstdlib>
 #include "kda_mx4_dev.h"
 #include "kda_mx4_internal.h"
 
 namespace kda {
 namespace {
 
-// The waves' sums joined in wave order, and stored.
-template <int RT, int WAVES>
-__device__ __forceinline__ void join(const Mx4Params& p, char* lds, const f32x4 (&acc)[RT], int n0, int64_t m0,
+// The waves' sums joined in wave order, and stored.  acc: tiles of 16 tokens (NT) by
+// tiles of 16 rows of w (RT).
+template <int NT, int RT, int WAVES>
+__device__ __forceinline__ void join(const Mx4Params& p, char* lds, const f32x4 (&acc)[NT][RT], int n0, int64_t m0,
                                      int lane, int wave) {
-  f32x4(*red)[RT][64] = reinterpret_cast<f32x4(*)[RT][64]>(lds);
+  constexpr int kTiles = NT * RT;
+  f32x4(*red)[kTiles][64] = reinterpret_cast<f32x4(*)[kTiles][64]>(lds);
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < RT; ++i) red[wave][i][lane] = acc[i];
+  for (int m = 0; m < NT; ++m)
+#pragma unroll
+    for (int i = 0; i < RT; ++i) red[wave][m * RT + i][lane] = acc[m][i];
   __syncthreads();
-  for (int t = threadIdx.x; t < RT * 256; t += 64 * WAVES) {
+  for (int t = threadIdx.x; t < kTiles * 256; t += 64 * WAVES) {
     // consecutive threads: consecutive rows of w of one token
-    const int r = t & 15, m = (t >> 4) & 15, i = t >> 8;
-    const float* at = reinterpret_cast<const float*>(&red[0][i][(r >> 2) * 16 + m]) + (r & 3);
+    const int r = t % (16 * RT), token = t / (16 * RT);
+    const int tile = (token >> 4) * RT + (r >> 4);
+    const float* at = reinterpret_cast<const float*>(&red[0][tile][((r & 15) >> 2) * 16 + (token & 15)]) + (r & 3);
     float y = at[0];
 #pragma unroll
-    for (int u = 1; u < WAVES; ++u) y += at[u * RT * 256];
-    const int n = n0 + 16 * i + r;
-    if (m0 + m < p.M && n < p.N) p.y[(m0 + m) * p.y_row + n] = f32_to_bf16(y);
+    for (int u = 1; u < WAVES; ++u) y += at[u * kTiles * 256];
+    if (m0 + token < p.M && n0 + r < p.N) p.y[(m0 + token) * p.y_row + n0 + r] = f32_to_bf16(y);
   }
 }
 
-template <int RQ, int RT, int WAVES, int STEPS>
-__global__ __launch_bounds__(64 * WAVES) void few_bf16_kernel(Mx4Params p) {
-  __shared__ __align__(16) char lds[WAVES * (4096 > RT * 1024 ? 4096 : RT * 1024)];
+// Units first .. end - 1 with U of them in flight.  (Loads only where a unit exists, so
+// that the compiler's waits cannot count them: loops whose waits can took as long, other
+// waves fill the time, and their extra loads cost the short calls.)
+template <int U, typename Unit, typename Load, typename Use>
+__device__ __forceinline__ void ring(Unit (&buf)[U], int first, int end, const Load& load, const Use& use) {
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (first + u < end) load(buf[u], first + u);
+  for (int unit = first; unit < end; unit += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (unit + u >= end) break;
+      use(buf[u], unit + u);
+      if (unit + u + U < end) load(buf[u], unit + u + U);
+    }
+  }
+}
+
+// Units first .. end - 1 with U of them in flight.  Where all of a round's loads exist
+// nothing is branched on, so that the waits count the loads behind the one they want.
+template <int U, typename Unit, typename Load, typename Use>
+__device__ __forceinline__ void counted_ring(Unit (&buf)[U], int first, int end, const Load& load, const Use& use) {
+  if (end - first < U) {
+    for (int unit = first; unit < end; ++unit) {
+      load(buf[0], unit);
+      use(buf[0], unit);
+    }
+    return;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(buf[u], first + u);
+  int unit = first;
+  for (; unit + 2 * U <= end; unit += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      use(buf[u], unit + u);
+      load(buf[u], unit + u + U);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    use(buf[u], unit + u);
+    if (unit + u + U < end) load(buf[u], unit + u + U);
+  }
+  unit += U;
+#pragma unroll
+  for (int u = 0; u < U - 1; ++u)
+    if (unit + u < end) use(buf[u], unit + u);
+}
+
+// NT tiles of 16 tokens (the first 4 RQ rows of each hold tokens), RT tiles of 16 rows of
+// w; U units of STEPS * 128 k in flight.
+template <int NT, int RQ, int RT, int WAVES, int STEPS, int U, bool TINY>
+__global__ __launch_bounds__(64 * WAVES, NT > 2 ? 2 : 4) void few_bf16_kernel(Mx4Params p) {
+  constexpr int kX = STEPS * NT * RQ * 1024, kWave = kX + RT * kPieceLds<STEPS>;
+  __shared__ __align__(16) char lds[WAVES * (kWave > NT * RT * 1024 ? kWave : NT * RT * 1024)];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * (16 * RT);
-  const int64_t m0 = int64_t(blockIdx.y) * 16;
+  const int n0 = blockIdx.x * (16 * RT), m0 = blockIdx.y * (16 * NT);
   const int nb = p.K / kMxBlock, units = (nb + 4 * STEPS - 1) / (4 * STEPS);
-  const int per = (units + WAVES - 1) / WAVES, first = wave * per, cnt = max(0, min(per, units - first));
+  const int first = units * wave / WAVES, end = units * (wave + 1) / WAVES;
   // rows behind the last row or token repeat it: their sums are not stored
-  const uint8_t *codes[RT], *scales[RT];
+  const uint8_t *codes = p.w + size_t(n0) * (p.K / 2), *scales = p.ws + size_t(n0) * nb;
+  uint32_t code_row[RT], scale_row[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
-    const size_t n = min(n0 + 16 * i + l16, p.N - 1);
-    codes[i] = p.w + n * (p.K / 2);
-    scales[i] = p.ws + n * nb;
+    const uint32_t r = min(16 * i + (lane >> 2), p.N - 1 - n0);
+    code_row[i] = r * (p.K / 2), scale_row[i] = r * nb;
   }
-  const uint16_t* row[RQ];
+  const uint16_t* x0 = static_cast<const uint16_t*>(p.x) + m0 * p.x_row;
+  uint32_t row[NT][RQ];
 #pragma unroll
-  for (int q = 0; q < RQ; ++q)
-    row[q] = static_cast<const uint16_t*>(p.x) + min(m0 + 4 * q + g, p.M - 1) * p.x_row;
-  char* xl = lds + wave * 4096;
-  f32x4 acc[RT] = {};
-  if (cnt) {
-    Piece<STEPS> buf[2][RT];
-    XRows<RQ> x;
-    const auto use = [&](Piece<STEPS>(&b)[RT], int unit) {
+  for (int m = 0; m < NT; ++m)
 #pragma unroll
-      for (int j = 0; j < STEPS; ++j) {
-        stage_x<RQ>(xl, x, l16, g);
-        load_x<RQ>(x, row, (unit * STEPS + j + 1) * 128, p.K, l16);
-        wave_lds_fence();
-        bf16x8 o[4];
+    for (int q = 0; q < RQ; ++q)
+      row[m][q] = uint32_t(min(16 * m + 4 * q + g, int(p.M) - 1 - m0)) * uint32_t(p.x_row * 2);
+  char *xl = lds + wave * kWave, *wl = xl + kX;
+  f32x4 acc[NT][RT] = {};
+  struct Unit {
+    Piece<STEPS> w[RT];
+    XRows<RQ> x[STEPS][NT];
+  } buf[U];
+  const auto load = [&](Unit& b, int unit) {
 #pragma unroll
-        for (int d = 0; d < 4; ++d) o[d] = x_operand(xl, d, l16, g);
+    for (int i = 0; i < RT; ++i)
+      load_piece<STEPS, TINY>(b.w[i], codes, code_row[i], scales, scale_row[i], nb, unit, lane & 3);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const float sc = scale_of(b[i].s[j], g);
+    for (int j = 0; j < STEPS; ++j)
 #pragma unroll
-          for (int d = 0; d < 4; ++d) acc[i] = mfma32(dequant8(b[i].w[j][d], sc), o[d], acc[i]);
-        }
-        wave_lds_fence();
+      for (int m = 0; m < NT; ++m) load_x<RQ>(b.x[j][m], x0, row[m], (unit * STEPS + j) * 128, p.K, l16);
+  };
+  const auto use = [&](Unit& b, int unit) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) stage_piece<STEPS, TINY>(wl + i * kPieceLds<STEPS>, b.w[i], nb, unit, lane);
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j)
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+        stage_x<RQ>(xl + (j * NT + m) * (RQ * 1024), b.x[j][m], (unit * STEPS + j) * 128, p.K, l16, g);
+    wave_lds_fence();
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+      bf16x8 w[RT][4];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const char* at = wl + i * kPieceLds<STEPS>;
+        const float sc = scale_of(scale_operand<STEPS>(at, j, l16, g));
+        const u32x4 c = codes_operand(at, j, l16, g);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) w[i][d] = dequant8(c[d], sc);
       }
-    };
-    const auto load = [&](Piece<STEPS>(&b)[RT], int unit) {
 #pragma unroll
-      for (int i = 0; i < RT; ++i) load_piece<STEPS>(b[i], codes[i], scales[i], nb, unit, g);
-    };
-    load(buf[0], first);
-    load_x<RQ>(x, row, first * STEPS * 128, p.K, l16);
-    int i = 0;
-    for (; i + 2 <= cnt; i += 2) {
-      load(buf[1], first + i + 1);
-      use(buf[0], first + i);
-      load(buf[0], first + min(i + 2, cnt - 1));
-      use(buf[1], first + i + 1);
+      for (int m = 0; m < NT; ++m)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const bf16x8 o = x_operand<RQ>(xl + (j * NT + m) * (RQ * 1024), d, l16, g);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) acc[m][i] = mfma32(w[i][d], o, acc[m][i]);
+        }
     }
-    if (i < cnt) use(buf[0], first + i);
-  }
-  join<RT, WAVES>(p, lds, acc, n0, m0, lane, wave);
+    wave_lds_fence();
+  };
+  ring<U>(buf, first, end, load, use);
+  join<NT, RT, WAVES>(p, lds, acc, n0, m0, lane, wave);
 }
 
-template <int RT, int WAVES, int STEPS>
-__global__ __launch_bounds__(64 * WAVES) void few_mx4_kernel(Mx4Params p) {
-  __shared__ __align__(16) char lds[WAVES * RT * 1024];
+// The same with x in the format too.
+template <int NT, int RT, int WAVES, int STEPS, int U, bool COUNTED, bool TINY>
+__global__ __launch_bounds__(64 * WAVES, COUNTED ? WAVES / 4 : 4) void few_mx4_kernel(Mx4Params p) {
+  constexpr int kWave = (NT + RT) * kPieceLds<STEPS>;
+  __shared__ __align__(16) char lds[WAVES * (kWave > NT * RT * 1024 ? kWave : NT * RT * 1024)];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int n0 = blockIdx.x * (16 * RT);
-  const int64_t m0 = int64_t(blockIdx.y) * 16;
+  const int64_t m0 = int64_t(blockIdx.y) * (16 * NT);
   const int nb = p.K / kMxBlock, units = (nb + 4 * STEPS - 1) / (4 * STEPS);
-  const int per = (units + WAVES - 1) / WAVES, first = wave * per, cnt = max(0, min(per, units - first));
-  const uint8_t *codes[RT], *scales[RT];
+  const int first = units * wave / WAVES, end = units * (wave + 1) / WAVES;
+  const uint8_t *codes = p.w + size_t(n0) * (p.K / 2), *scales = p.ws + size_t(n0) * nb;
+  const uint8_t *xc = static_cast<const uint8_t*>(p.x) + size_t(m0) * (p.K / 2), *xs = p.xs + size_t(m0) * nb;
+  uint32_t code_row[RT], scale_row[RT], x_row[NT], xs_row[NT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
-    const size_t n = min(n0 + 16 * i + l16, p.N - 1);
-    codes[i] = p.w + n * (p.K / 2);
-    scales[i] = p.ws + n * nb;
+    const uint32_t r = min(16 * i + (lane >> 2), p.N - 1 - n0);
+    code_row[i] = r * (p.K / 2), scale_row[i] = r * nb;
   }
-  const size_t m = size_t(min(m0 + l16, p.M - 1));
-  const uint8_t *xc = static_cast<const uint8_t*>(p.x) + m * (p.K / 2), *xs = p.xs + m * nb;
-  f32x4 acc[RT] = {};
-  if (cnt) {
-    Piece<STEPS> buf[2][RT], x[2];
-    const auto use = [&](Piece<STEPS>(&b)[RT], Piece<STEPS>& x) {
+  const int last = int(p.M - 1 - m0 < 16 * NT ? p.M - 1 - m0 : 16 * NT - 1);
 #pragma unroll
-      for (int j = 0; j < STEPS; ++j)
+  for (int m = 0; m < NT; ++m) {
+    const uint32_t r = min(16 * m + (lane >> 2), last);
+    x_row[m] = r * (p.K / 2), xs_row[m] = r * nb;
+  }
+  f32x4 acc[NT][RT] = {};
+  struct Unit {
+    Piece<STEPS> w[RT], x[NT];
+  } buf[U];
+  const auto load = [&](Unit& b, int unit) {
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-          acc[i] = mfma_mx4(b[i].w[j], b[i].s[j] >> (8 * g), x.w[j], x.s[j] >> (8 * g), acc[i]);
-    };
-    const auto load = [&](Piece<STEPS>(&b)[RT], Piece<STEPS>& x, int unit) {
+    for (int i = 0; i < RT; ++i)
+      load_piece<STEPS, TINY>(b.w[i], codes, code_row[i], scales, scale_row[i], nb, unit, lane & 3);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) load_piece<STEPS>(b[i], codes[i], scales[i], nb, unit, g);
-      load_piece<STEPS>(x, xc, xs, nb, unit, g);
-    };
-    load(buf[0], x[0], first);
-    int i = 0;
-    for (; i + 2 <= cnt; i += 2) {
-      load(buf[1], x[1], first + i + 1);
-      use(buf[0], x[0]);
-      load(buf[0], x[0], first + min(i + 2, cnt - 1));
-      use(buf[1], x[1]);
+    for (int m = 0; m < NT; ++m) load_piece<STEPS, TINY>(b.x[m], xc, x_row[m], xs, xs_row[m], nb, unit, lane & 3);
+  };
+  char *wl = lds + wave * kWave, *xl = wl + RT * kPieceLds<STEPS>;
+  const auto use = [&](Unit& b, int unit) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) stage_piece<STEPS, TINY>(wl + i * kPieceLds<STEPS>, b.w[i], nb, unit, lane);
+#pragma unroll
+    for (int m = 0; m < NT; ++m) stage_piece<STEPS, TINY>(xl + m * kPieceLds<STEPS>, b.x[m], nb, unit, lane);
+    wave_lds_fence();
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+      u32x4 w[RT];
+      uint32_t sw[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        w[i] = codes_operand(wl + i * kPieceLds<STEPS>, j, l16, g);
+        sw[i] = scale_operand<STEPS>(wl + i * kPieceLds<STEPS>, j, l16, g);
+      }
+#pragma unroll
+      for (int m = 0; m < NT; ++m) {
+        const u32x4 x = codes_operand(xl + m * kPieceLds<STEPS>, j, l16, g);
+        const uint32_t sx = scale_operand<STEPS>(xl + m * kPieceLds<STEPS>, j, l16, g);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[m][i] = mfma_mx4(w[i], sw[i], x, sx, acc[m][i]);
+      }
     }
-    if (i < cnt) use(buf[0], x[0]);
-  }
-  join<RT, WAVES>(p, lds, acc, n0, m0, lane, wave);
+    wave_lds_fence();
+  };
+  if (COUNTED)
+    counted_ring<U>(buf, first, end, load, use);
+  else
+    ring<U>(buf, first, end, load, use);
+  join<NT, RT, WAVES>(p, lds, acc, n0, m0, lane, wave);
 }
 
-template <int RT, int WAVES>
-hipError_t launch(const void* f, const Mx4Params& p, hipStream_t st) {
+// Grid: tiles of w's rows by tiles of tokens.
+hipError_t go(const void* f, int nt, int rt, int waves, const Mx4Params& p, hipStream_t st) {
   Mx4Params arg = p;
   void* args[] = {&arg};
-  const dim3 grid((p.N + 16 * RT - 1) / (16 * RT), uint32_t((p.M + 15) / 16));
-  return hipLaunchKernel(f, grid, dim3(64 * WAVES), args, 0, st);
+  const dim3 grid((p.N + 16 * rt - 1) / (16 * rt), uint32_t((p.M + 16 * nt - 1) / (16 * nt)));
+  return hipLaunchKernel(f, grid, dim3(64 * waves), args, 0, st);
+}
+
+template <int NT, int RQ, int RT, int WAVES, int STEPS, int U>
+hipError_t few_bf16(const Mx4Params& p, hipStream_t st) {
+  const auto at = [](auto* f) { return reinterpret_cast<const void*>(f); };
+  return go(p.K < 128 ? at(&few_bf16_kernel<NT, RQ, RT, WAVES, STEPS, U, true>)
+                              : at(&few_bf16_kernel<NT, RQ, RT, WAVES, STEPS, U, false>),
+            NT, RT, WAVES, p, st);
+}
+template <int NT, int RT, int WAVES, int STEPS, int U, bool COUNTED = false>
+hipError_t few_mx4(const Mx4Params& p, hipStream_t st) {
+  const auto at = [](auto* f) { return reinterpret_cast<const void*>(f); };
+  return go(p.K < 128 ? at(&few_mx4_kernel<NT, RT, WAVES, STEPS, U, COUNTED, true>)
+                              : at(&few_mx4_kernel<NT, RT, WAVES, STEPS, U, COUNTED, false>),
+            NT, RT, WAVES, p, st);
 }
 
 }  // namespace
 
 hipError_t launch_mx4_few(const Mx4Params& p, int cus, hipStream_t stream) {
-  if (p.xs) return launch<2, 8>(reinterpret_cast<const void*>(&few_mx4_kernel<2, 8, 2>), p, stream);
-  if (p.M <= 4) return launch<1, 8>(reinterpret_cast<const void*>(&few_bf16_kernel<1, 1, 8, 2>), p, stream);
-  return launch<2, 8>(reinterpret_cast<const void*>(&few_bf16_kernel<4, 2, 8, 2>), p, stream);
+  static const int v = [] { const char* e = getenv("MXV"); return e ? atoi(e) : 0; }();
+  if (p.xs) {
+    if (p.M <= 16) {
+      if (v == 1) return few_mx4<1, 1, 8, 2, 2>(p, stream);
+      if (v == 2) return few_mx4<1, 2, 8, 1, 3>(p, stream);
+      if (v == 3) return few_mx4<1, 1, 16, 2, 2>(p, stream);
+      if (v == 4) return few_mx4<1, 2, 16, 2, 1>(p, stream);
+      return few_mx4<1, 2, 8, 2, 2>(p, stream);
+    }
+    if (v == 1) return few_mx4<2, 2, 8, 2, 1>(p, stream);
+    if (v == 2) return few_mx4<4, 4, 4, 1, 4, true>(p, stream);
+    if (v == 3) return few_mx4<4, 4, 8, 1, 2, true>(p, stream);
+    if (v == 4) return few_mx4<4, 4, 8, 1, 1>(p, stream);
+    if (v == 5) return few_mx4<2, 4, 4, 1, 4, true>(p, stream);
+    if (v == 6) return few_mx4<2, 4, 8, 1, 2, true>(p, stream);
+    if (v == 7) return few_mx4<2, 2, 4, 1, 4, true>(p, stream);
+    return few_mx4<2, 2, 8, 1, 2>(p, stream);
+  }
+  if (p.M <= 4) {
+    if (v == 1) return few_bf16<1, 1, 1, 16, 2, 2>(p, stream);
+    if (v == 2) return few_bf16<1, 1, 2, 8, 2, 2>(p, stream);
+    if (v == 3) return few_bf16<1, 1, 1, 8, 1, 4>(p, stream);
+    if (v == 4) return few_bf16<1, 1, 1, 16, 1, 4>(p, stream);
+    return few_bf16<1, 1, 1, 8, 2, 2>(p, stream);
+  }
+  if (p.M <= 16) {
+    if (v == 1) return few_bf16<1, 4, 2, 8, 1, 3>(p, stream);
+    if (v == 2) return few_bf16<1, 4, 1, 8, 1, 2>(p, stream);
+    if (v == 3) return few_bf16<1, 4, 2, 16, 1, 2>(p, stream);
+    if (v == 4) return few_bf16<1, 4, 4, 8, 1, 1>(p, stream);
+    return few_bf16<1, 4, 2, 8, 1, 2>(p, stream);
+  }
+  if (v == 1) return few_bf16<4, 4, 2, 8, 1, 1>(p, stream);
+  if (v == 2) return few_bf16<2, 4, 2, 8, 1, 1>(p, stream);
+  if (v == 3) return few_bf16<4, 4, 1, 8, 1, 1>(p, stream);
+  if (v == 4) return few_bf16<2, 4, 1, 8, 1, 1>(p, stream);
+  return few_bf16<1, 4, 2, 8, 1, 2>(p, stream);
 }
 
 }  // namespace kda

@@ -31,8 +31,13 @@ bool mx4_tile_ok(const Mx4Params& p);
 hipError_t launch_mx4_tile(const Mx4Params& p, int cus, hipStream_t stream);
 
 // One call of the mixture-of-experts layer.  A pair is a token and an expert that
-// it goes through; pairs are listed by expert, then token.  A slot is an expert
-// that is hit.
+// it goes through; pairs are numbered by expert, then token.  A slot is an expert and
+// up to `chunk` of its tokens.
+struct MoeSlot {
+  int32_t expert, begin, n, unused;  // pairs begin .. begin + n - 1
+  uint32_t token[4];                 // 16 bytes: the pairs' tokens, the last repeated
+};
+
 struct MoeParams {
   const uint16_t *x, *router;
   const float* bias;
@@ -45,20 +50,27 @@ struct MoeParams {
   int M, K, I, E, S, top;
   int softmax, renorm;
   float route_scale;
-  // workspace
+  int chunk;                 // tokens per slot: 4 or 16
   int slices, slice_blocks;  // of the router's sums over k: how many, of how many 32s
-  double* logits;       // [slices][M][E]
-  int32_t* head;        // [0]: tokens routed so far, [1]: slots in use
-  int32_t* slot_expert; // [slots]
-  int32_t* slot_begin;  // [slots + 1] into pairs
-  int32_t* pairs;       // [M (top + S)]: the pair's token
-  float* pair_gate;     // [M (top + S)]
+  int up_log2;               // of up's workgroups
+  int parts;                 // into which down's sum over slots is cut
+  // workspace
+  double* logits;         // [slices][M][E]
+  int32_t* head;          // [0]: tokens routed so far, [1]: slots in use
+  int32_t* done;          // [K / 16]: parts of down's sums that are there
+  MoeSlot* slot;
+  float* pair_gate;       // [M (top + S) + 16]
   uint16_t *h_hi, *h_lo;  // [M (top + S)][I]: silu(G x) * (U x) as two bf16 pieces
+  float* sums;            // [parts][M][K]
 };
 struct MoeLayout {
-  int slices, slice_blocks, slots;
-  size_t logits, head, slot_expert, slot_begin, pairs, pair_gate, h_hi, h_lo, total;
+  int slices, slice_blocks;
+  size_t logits, head, done, slot, pair_gate, h_hi, h_lo, sums, total;
 };
+// Slots that a call may have, at most.
+int moe_slots(int M, int E, int S, int top, int chunk);
+int moe_parts(int M, int K, int I, int E, int S, int top, int chunk);
+constexpr int kMoeMostParts = 8;
 MoeLayout moe_layout(int M, int K, int I, int E, int S, int top);
 hipError_t launch_moe(const MoeParams& p, int cus, hipStream_t stream);
 

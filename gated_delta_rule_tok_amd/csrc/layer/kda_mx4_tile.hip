@@ -2,18 +2,18 @@
 // 4-bit numbers:  y[m, n] = sum_k x[m, k] w[n, k].
 //
 // Bound by the scaled 4-bit MFMA (32x32x64: 32 cycles).  A workgroup of four waves
-// makes BM x BN outputs, each wave a quarter, from operands in LDS: four stages of
-// 128 of k that loads fill directly, three ahead of the one in use, and the scales
-// of 512 of k at a time.  A wave of 128 x 128 outputs reads 8 KB of LDS for 16
-// MFMAs, 64 of LDS's 128 bytes a cycle with four waves.
-//
-// LDS holds a row's 64 bytes of a stage as four pieces of 16, at piece ^ (row / 2)
-// % 4, so that 8 adjacent rows' pieces are in different banks; a load into LDS
-// places lanes in order, so the permutation is made by the addresses that it reads.
+// makes BM x BN outputs, each wave a quarter, from operands in LDS: stages of 128 of k
+// that loads fill directly, three or seven ahead of the one in use, and the scales of
+// 512 of k at a time.  A wave of 128 x 128 outputs reads 8 KB of LDS for 16 MFMAs, 64 of
+// LDS's 128 bytes a cycle with four waves; it has the operands of its next 16 MFMAs on
+// the way while it issues 16, over the barrier between stages too.
 //
 // The loads are written in assembly: with the builtin the compiler waits for every
 // load into LDS before each read of it, which leaves one stage in flight.  Their
-// count in flight is waited on by hand (see Stage).
+// count in flight is waited on by hand.
+#include <cstdlib>
+#include <type_traits>
+
 #include "kda_mx4_dev.h"
 #include "kda_mx4_internal.h"
 
@@ -23,13 +23,11 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kStages = 4;
-
-// 16 bytes per lane from base + soff + voff to LDS at lds + 16 * lane
-__device__ __forceinline__ void load_lds(i32x4 base, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :: "s"(lds), "v"(voff), "s"(base), "s"(soff)
-               : "memory");
+// 16 bytes per lane from base + soff + voff to LDS at lds + more + 16 * lane
+__device__ __forceinline__ void load_lds(i32x4 base, uint32_t voff, uint32_t soff, uint32_t lds, uint32_t more) {
+  asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :: "s"(lds), "v"(voff), "s"(base), "s"(soff), "i"(more)
+               : "memory", "scc");
 }
 __device__ __forceinline__ i32x4 rsrc_of(const void* p) {
   const uint64_t a = reinterpret_cast<uint64_t>(p);
@@ -40,18 +38,28 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)(p)));
 }
 
-template <int BM, int BN>
+// NS stages of 128 of k; scales of 512 of k for those in flight and the one in use
+template <int BM, int BN, int NS>
 struct TileLds {
-  char code[kStages][(BM + BN) * 64];  // x's rows, then w's
-  char scale[2][(BM + BN) * 16];
+  static constexpr int kScales = NS == 4 ? 2 : 4;
+  char code[NS][(BM + BN) * 64];  // x's rows, then w's
+  char scale[kScales][(BM + BN) * 16];
 };
 
-template <int BM, int BN>
-__global__ __launch_bounds__(256, 1) void tile_kernel(Mx4Params p) {
-  constexpr int FM = BM / 64, FN = BN / 64;          // 32 x 32 tiles of a wave, either way
-  constexpr int kLoads = (BM + BN) / 64;             // per wave and stage
-  constexpr int kScaleLoads = (BM + BN) / 256;       // per wave and four stages
-  __shared__ __align__(16) TileLds<BM, BN> L;
+template <int N>
+__device__ __forceinline__ void wait_loads() {  // at most N loads under way, and none from LDS
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(N) : "memory");
+}
+
+// WN: waves along w's rows; two along x's
+template <int BM, int BN, int NS, int WN>
+__global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
+  constexpr int kWaves = 2 * WN;
+  constexpr int FM = BM / 64, FN = BN / (32 * WN);          // 32 x 32 tiles of a wave, either way
+  constexpr int kLoads = (BM + BN) / (16 * kWaves);         // per wave and stage
+  constexpr int kScaleLoads = (BM + BN) / (64 * kWaves);    // per wave and four stages
+  static_assert(kScaleLoads * 64 * kWaves == BM + BN, "");
+  __shared__ __align__(16) TileLds<BM, BN, NS> L;
   char* smem = L.code[0];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, half = lane >> 5;
@@ -77,7 +85,7 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(Mx4Params p) {
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const int r = (wave * kLoads + i) * 16 + (lane >> 2);  // row of the stage
-    const uint32_t piece = ((lane & 3) ^ (r >> 1)) & 3;
+    const uint32_t piece = (lane & 3) ^ bank_turn(r);
     off[i] = uint32_t(r < BM ? min(r, mlast) : min(r - BM, nlast)) * row_bytes + piece * 16;
   }
 #pragma unroll
@@ -86,83 +94,131 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(Mx4Params p) {
     soff[i] = uint32_t(r < BM ? min(r, mlast) : min(r - BM, nlast)) * nb;
   }
   const int T = p.K / 128;
-  const uint32_t code0 = lds_address(L.code[0]), scale0 = lds_address(L.scale[0]);
+  // (a wave's loads are all of x or all of w)
+  static_assert(BM == BN, "");
+  const i32x4 code_base = wave < kWaves / 2 ? xb : wb, scale_base = wave < kWaves / 2 ? xsb : wsb;
+  const uint32_t code0 = lds_address(L.code[0]) + wave * (kLoads * 1024),
+                 scale0 = lds_address(L.scale[0]) + wave * (kScaleLoads * 1024);
+  // Stages behind the last are loaded too, from where the last one is: a loop without
+  // branches whose waits count the same loads every time.
+  const auto issue = [&](int t, int i) {
+    load_lds(code_base, off[i], min(t, T - 1) * 64, code0 + (t & (NS - 1)) * sizeof(L.code[0]), i * 1024);
+  };
   // The scales of four stages are 16 bytes a row; the last ones of a row are its last
   // 16 bytes, so that no load passes its end.
-  const auto issue = [&](int t) {
-    if ((t & 3) == 0) {
+  const auto issue_scales = [&](int t) {
+    if ((t & 3) || t >= T) return;
 #pragma unroll
-      for (int i = 0; i < kScaleLoads; ++i) {
-        const int c = wave * kScaleLoads + i;
-        load_lds(c * 64 < BM ? xsb : wsb, soff[i], min(uint32_t(4 * t), nb - 16),
-                 scale0 + ((t >> 2) & 1) * sizeof(L.scale[0]) + c * 1024);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int c = wave * kLoads + i;
-      load_lds(c * 16 < BM ? xb : wb, off[i], t * 64, code0 + (t & 3) * sizeof(L.code[0]) + c * 1024);
+    for (int i = 0; i < kScaleLoads; ++i) {
+      load_lds(scale_base, soff[i], min(uint32_t(4 * t), nb - 16),
+               scale0 + ((t >> 2) & (L.kScales - 1)) * sizeof(L.scale[0]), i * 1024);
     }
   };
   f32x16 acc[FM][FN] = {};
-  const int xr = (wave >> 1) * (BM / 2) + l32, wr = BM + (wave & 1) * (BN / 2) + l32;  // rows of the stage
-  issue(0);
-  if (T > 1) issue(1);
-  if (T > 2) issue(2);
+  const int xr = wave / WN * (BM / 2) + l32, wr = BM + wave % WN * (BN / WN) + l32;  // rows of the stage
+  struct Frags {
+    u32x4 a[FN], b[FM];
+  } f[2];
+  struct Scales {
+    uint32_t x[FM], w[FN];
+  } sc;
+  // fragment i of stage t, half s (0, 1): w's, then x's
+  const auto read = [&](Frags& f, int t, int s, int i) {
+    const int r = i < FN ? wr + 32 * i : xr + 32 * (i - FN);
+    const u32x4 v = *reinterpret_cast<const u32x4*>(L.code[t & (NS - 1)] + r * 64 + ((2 * s + half) ^ bank_turn(r)) * 16);
+    if (i < FN)
+      f.a[i] = v;
+    else
+      f.b[i - FN] = v;
+  };
+  const auto read_scale = [&](Scales& o, int t, int i) {
+    t = min(t, T - 1);
+    const int at = 4 * t - int(min(uint32_t(4 * (t & ~3)), nb - 16));  // this stage's in the row's 16 bytes
+    const int r = i < FN ? wr + 32 * i : xr + 32 * (i - FN);
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(L.scale[(t >> 2) & (L.kScales - 1)] + at + r * 16);
+    if (i < FN)
+      o.w[i] = v;
+    else
+      o.x[i - FN] = v;
+  };
+  // The products of one half stage; between(n) is issued behind the n-th of them: a wave
+  // alone on its SIMD issues everything else in the MFMAs' time or instead of them.
+  const auto multiply = [&](const Frags& f, auto s, const Scales& c, const auto& between) {
+    constexpr int kByte = 2 * decltype(s)::value;  // of the shifted scales
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            codes8(f.a[j]), codes8(f.b[i]), acc[i][j], 4, 4, kByte, int(c.w[j]), kByte, int(c.x[i]));
+        __builtin_amdgcn_sched_barrier(0);
+        between(i * FN + j);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+  };
+#pragma unroll
+  for (int t = 0; t < NS; ++t) {
+    issue_scales(t);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      if (t + 1 < NS || i < kLoads - kLoads / 2) issue(t, i);  // (the rest comes in the loop)
+  }
+  wait_loads<(NS - 2) * kLoads>();  // the first stage
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  constexpr int kReads = FN + FM, kSlots = FM * FN;  // fragments of a half stage; MFMAs
+#pragma unroll
+  for (int i = 0; i < kReads; ++i) {
+    read(f[0], 0, 0, i);
+    read_scale(sc, 0, i);
+  }
+  const auto shift = [&](Scales& c) {
+#pragma unroll
+    for (int i = 0; i < FN; ++i) c.w[i] >>= 8 * half;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) c.x[i] >>= 8 * half;
+  };
+  shift(sc);
+  // Reads in the first half of a half stage's MFMAs, loads in the second half: those of
+  // stage t + NS where stage t's last read is done, the rest in front of the next wait.
+  constexpr int kEach = (2 * kReads + kSlots - 1) / kSlots, kLoadsEach = (kLoads + kSlots - 1) / kSlots;
+  constexpr int kLate = kLoads / 2;  // of a stage's loads, in the next one's time
   for (int t = 0; t < T; ++t) {
-    // stage t is in LDS: the loads of the two stages behind it may be under way; and
-    // what this wave read of stage t - 1 has arrived, so that it may be overwritten
-    if (t + 2 < T) {
-      if (kLoads == 8)
-        asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)" ::: "memory");
-      else
-        asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)" ::: "memory");
-    } else {
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    }
+    // (the one branch, in front: the compiler moves MFMAs behind one, all at once)
+    if (t) issue_scales(t + NS - 1);
+    multiply(f[0], std::integral_constant<int, 0>{}, sc, [&](int n) {
+#pragma unroll
+      for (int i = n * kEach; i < (n + 1) * kEach && i < kReads; ++i) read(f[1], t, 1, i);
+#pragma unroll
+      for (int i = (n - kSlots / 2) * kLoadsEach; i < (n - kSlots / 2 + 1) * kLoadsEach; ++i)
+        if (i >= 0 && i < kLate) issue(t + NS - 1, kLoads - kLate + i);
+    });
+    // stage t + 1 is in LDS (those behind it may be under way), and every wave has read
+    // all of stage t, which the loads may overwrite
+    wait_loads<(NS - 2) * kLoads>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (t + 3 < T) issue(t + 3);  // into the stage that every wave has left
-    const char* code = L.code[t & 3];
-    const int sd = 4 * t - int(min(uint32_t(4 * (t & ~3)), nb - 16));  // this stage's scales in the row's 16 bytes
-    const char* scale = L.scale[(t >> 2) & 1] + sd;
-    uint32_t sx[FM], sw[FN];
+    Scales next;
+    multiply(f[1], std::integral_constant<int, 1>{}, sc, [&](int n) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) sx[i] = *reinterpret_cast<const uint32_t*>(scale + (xr + 32 * i) * 16) >> (8 * half);
-#pragma unroll
-    for (int i = 0; i < FN; ++i) sw[i] = *reinterpret_cast<const uint32_t*>(scale + (wr + 32 * i) * 16) >> (8 * half);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      u32x4 a[FN], b[FM];
-#pragma unroll
-      for (int i = 0; i < FN; ++i) {
-        const int r = wr + 32 * i;
-        a[i] = *reinterpret_cast<const u32x4*>(code + r * 64 + (((2 * s + half) ^ (r >> 1)) & 3) * 16);
+      for (int i = n * kEach; i < (n + 1) * kEach && i < kReads; ++i) {
+        read(f[0], t + 1, 0, i);
+        read_scale(next, t + 1, i);
       }
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int r = xr + 32 * i;
-        b[i] = *reinterpret_cast<const u32x4*>(code + r * 64 + (((2 * s + half) ^ (r >> 1)) & 3) * 16);
-      }
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          if (s == 0)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(codes8(a[j]), codes8(b[i]), acc[i][j], 4, 4, 0,
-                                                                        int(sw[j]), 0, int(sx[i]));
-          else
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(codes8(a[j]), codes8(b[i]), acc[i][j], 4, 4, 2,
-                                                                        int(sw[j]), 2, int(sx[i]));
-        }
-    }
+      for (int i = (n - kSlots / 2) * kLoadsEach; i < (n - kSlots / 2 + 1) * kLoadsEach; ++i)
+        if (i >= 0 && i < kLoads - kLate) issue(t + NS, i);
+    });
+    shift(next);
+    sc = next;
   }
+  wait_loads<0>();
   // y by rows of 16-byte pieces, through LDS: 32 tokens of this wave at a time
   __syncthreads();
-  constexpr int kPitch = BN / 2 * 2 + 16;  // bytes
+  constexpr int kPitch = BN / WN * 2 + 16;  // bytes
   char* mine = smem + wave * 32 * kPitch;
-  const int64_t mw = m0 + (wave >> 1) * (BM / 2);
-  const int nw = n0 + (wave & 1) * (BN / 2);
+  const int64_t mw = m0 + wave / WN * (BM / 2);
+  const int nw = n0 + wave % WN * (BN / WN);
   const bool vec = p.y_row % 8 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
@@ -175,7 +231,7 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(Mx4Params p) {
         *reinterpret_cast<bf16x4*>(mine + l32 * kPitch + (32 * j + 8 * q + 4 * half) * 2) = to_bf16x4(v);
       }
     wave_lds_fence();
-    constexpr int kPieces = BN / 16;  // 16-byte pieces of a token
+    constexpr int kPieces = BN / WN / 8;  // 16-byte pieces of a token
 #pragma unroll
     for (int q = 0; q < 32 * kPieces / 64; ++q) {
       const int at = q * 64 + lane, r = at / kPieces, c = at % kPieces;
@@ -196,13 +252,13 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(Mx4Params p) {
   }
 }
 
-template <int BM, int BN>
+template <int BM, int BN, int NS, int WN>
 hipError_t launch(const Mx4Params& p, hipStream_t st) {
-  const void* f = reinterpret_cast<const void*>(&tile_kernel<BM, BN>);
+  const void* f = reinterpret_cast<const void*>(&tile_kernel<BM, BN, NS, WN>);
   Mx4Params arg = p;
   void* args[] = {&arg};
   const int64_t tiles = ((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
-  return hipLaunchKernel(f, dim3(uint32_t(tiles)), dim3(256), args, 0, st);
+  return hipLaunchKernel(f, dim3(uint32_t(tiles)), dim3(128 * WN), args, 0, st);
 }
 
 }  // namespace
@@ -214,8 +270,11 @@ bool mx4_tile_ok(const Mx4Params& p) {
 
 hipError_t launch_mx4_tile(const Mx4Params& p, int cus, hipStream_t stream) {
   const int64_t big = ((p.M + 255) / 256) * ((p.N + 255) / 256);
-  if (2 * big > cus) return launch<256, 256>(p, stream);
-  return launch<128, 128>(p, stream);
+  static const int v = [] { const char* e = getenv("MXT"); return e ? atoi(e) : 0; }();
+  if (v ? v == 2 : 2 * big > cus) return launch<256, 256, 4, 2>(p, stream);
+  if (v == 3) return launch<256, 256, 4, 4>(p, stream);
+  if (v == 4) return launch<128, 128, 8, 1>(p, stream);
+  return launch<128, 128, 8, 2>(p, stream);
 }
 
 }  // namespace kda
