@@ -14,7 +14,6 @@
 // sum, and with a whole-number result there is no rounding to hide behind.  It
 // costs 0.75 us of the fp64 matrix pipe per 16 tokens at 256 x 7168.
 #include <type_traits>
-#include <cstdlib>
 
 #include "kda_mx4_dev.h"
 #include "kda_mx4_internal.h"
@@ -691,8 +690,7 @@ hipError_t launch_moe(const MoeParams& params, int cus, hipStream_t st) {
   MoeParams p = params;
   // Tokens per slot: 4 where an expert that is hit has about two.  Those with more are
   // read once for each 4 (from the L2, by workgroups that run at the same time).
-  static const int v = [] { const char* e = getenv("MXC"); return e ? atoi(e) : 2; }();
-  p.chunk = p.M <= 4 || p.M * p.top <= v * p.E ? 4 : 16;
+  p.chunk = p.M <= 4 || p.M * p.top <= 2 * p.E ? 4 : 16;
   p.parts = moe_parts(p.M, p.K, p.I, p.E, p.S, p.top, p.chunk);
   void* args[] = {&p};
   const auto go = [&](auto* f, dim3 grid, int threads, size_t lds) {

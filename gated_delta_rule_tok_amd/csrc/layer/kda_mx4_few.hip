@@ -8,7 +8,6 @@
 // MFMA as it is; with x in bf16 the codes become bf16 (an exact conversion, the
 // scale applied) and four MFMAs take the lane's four dwords in turn, x's operand
 // in the same order of k.
-#include <cstdlib>
 #include "kda_mx4_dev.h"
 #include "kda_mx4_internal.h"
 
@@ -56,38 +55,6 @@ __device__ __forceinline__ void ring(Unit (&buf)[U], int first, int end, const L
       if (unit + u + U < end) load(buf[u], unit + u + U);
     }
   }
-}
-
-// Units first .. end - 1 with U of them in flight.  Where all of a round's loads exist
-// nothing is branched on, so that the waits count the loads behind the one they want.
-template <int U, typename Unit, typename Load, typename Use>
-__device__ __forceinline__ void counted_ring(Unit (&buf)[U], int first, int end, const Load& load, const Use& use) {
-  if (end - first < U) {
-    for (int unit = first; unit < end; ++unit) {
-      load(buf[0], unit);
-      use(buf[0], unit);
-    }
-    return;
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) load(buf[u], first + u);
-  int unit = first;
-  for (; unit + 2 * U <= end; unit += U) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      use(buf[u], unit + u);
-      load(buf[u], unit + u + U);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    use(buf[u], unit + u);
-    if (unit + u + U < end) load(buf[u], unit + u + U);
-  }
-  unit += U;
-#pragma unroll
-  for (int u = 0; u < U - 1; ++u)
-    if (unit + u < end) use(buf[u], unit + u);
 }
 
 // NT tiles of 16 tokens (the first 4 RQ rows of each hold tokens), RT tiles of 16 rows of
@@ -167,8 +134,8 @@ __global__ __launch_bounds__(64 * WAVES, NT > 2 ? 2 : 4) void few_bf16_kernel(Mx
 }
 
 // The same with x in the format too.
-template <int NT, int RT, int WAVES, int STEPS, int U, bool COUNTED, bool TINY>
-__global__ __launch_bounds__(64 * WAVES, COUNTED ? WAVES / 4 : 4) void few_mx4_kernel(Mx4Params p) {
+template <int NT, int RT, int WAVES, int STEPS, int U, bool TINY>
+__global__ __launch_bounds__(64 * WAVES, 4) void few_mx4_kernel(Mx4Params p) {
   constexpr int kWave = (NT + RT) * kPieceLds<STEPS>;
   __shared__ __align__(16) char lds[WAVES * (kWave > NT * RT * 1024 ? kWave : NT * RT * 1024)];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -228,10 +195,7 @@ __global__ __launch_bounds__(64 * WAVES, COUNTED ? WAVES / 4 : 4) void few_mx4_k
     }
     wave_lds_fence();
   };
-  if (COUNTED)
-    counted_ring<U>(buf, first, end, load, use);
-  else
-    ring<U>(buf, first, end, load, use);
+  ring<U>(buf, first, end, load, use);
   join<NT, RT, WAVES>(p, lds, acc, n0, m0, lane, wave);
 }
 
@@ -250,54 +214,49 @@ hipError_t few_bf16(const Mx4Params& p, hipStream_t st) {
                               : at(&few_bf16_kernel<NT, RQ, RT, WAVES, STEPS, U, false>),
             NT, RT, WAVES, p, st);
 }
-template <int NT, int RT, int WAVES, int STEPS, int U, bool COUNTED = false>
+template <int NT, int RT, int WAVES, int STEPS, int U>
 hipError_t few_mx4(const Mx4Params& p, hipStream_t st) {
   const auto at = [](auto* f) { return reinterpret_cast<const void*>(f); };
-  return go(p.K < 128 ? at(&few_mx4_kernel<NT, RT, WAVES, STEPS, U, COUNTED, true>)
-                              : at(&few_mx4_kernel<NT, RT, WAVES, STEPS, U, COUNTED, false>),
+  return go(p.K < 128 ? at(&few_mx4_kernel<NT, RT, WAVES, STEPS, U, true>)
+                              : at(&few_mx4_kernel<NT, RT, WAVES, STEPS, U, false>),
             NT, RT, WAVES, p, st);
 }
 
 }  // namespace
 
+// Which form, measured on 256 compute units (us):
+//  * Rows of w per workgroup: 16 give the most workgroups, 32 read x half as often.
+//    bf16, 16 / 32: 16 x 7168 x 1536 6.6 / 8.4, 16 x 2048 x 4096 3.8 / 4.5, 16 x 7168 x
+//    7168 15.1 / 12.7; so 16 up to 384 workgroups.  64 where they still are 154 and more:
+//    16 x 4096 x 10240 12.1 against 13.0, 16 x 7168 x 14336 20.2 / 22.3, but 16 x 7168 x
+//    7168 18.0 / 12.7.  With x in the format 16 up to 192 workgroups of 32: 16 x 7168 x
+//    1536 4.4 / 5.9, 16 x 7168 x 7168 9.5 / 9.2.
+//  * At most 4 tokens: 16 waves share k where the workgroups are half the units or fewer
+//    (1 x 7168 x 1536 4.3 against 4.8 with 8, 1 x 2048 x 4096 3.4 / 3.1), 32 rows where
+//    those of 16 are three times the units (1 x 7168 x 14336 13.9 against 14.5).
+//  * Tokens per workgroup: 16, which for more tokens reads w again, from the L2 or the
+//    cache behind it; 32 and 64 hold x of a step in registers, so that fewer waves run.
+//    64: 61 x 2080 x 7171 10.6 against 12.4 with 16, 64 x 7168 x 7168 24.0 / 27.9, but 48 x
+//    2048 x 7168 9.1 / 8.4, 64 x 2048 x 2048 8.8 / 4.6.  32: 30 x 7168 x 14336 29.4 / 33.4,
+//    but 32 x 7168 x 1536 11.9 / 8.1.  With x in the format 32 and one unit in flight for
+//    all of more than 16 tokens: 64 x 7168 x 1536 7.4 against 8.2 with 32 rows in two
+//    units, 17.7 with 64 x 64; 300 x 4128 x 2050 16.1 / 19.4 / 18.0.
 hipError_t launch_mx4_few(const Mx4Params& p, int cus, hipStream_t stream) {
-  static const int v = [] { const char* e = getenv("MXV"); return e ? atoi(e) : 0; }();
+  const int64_t rows16 = (p.N + 15) / 16, rows32 = (p.N + 31) / 32, rows64 = (p.N + 63) / 64;
   if (p.xs) {
-    if (p.M <= 16) {
-      if (v == 1) return few_mx4<1, 1, 8, 2, 2>(p, stream);
-      if (v == 2) return few_mx4<1, 2, 8, 1, 3>(p, stream);
-      if (v == 3) return few_mx4<1, 1, 16, 2, 2>(p, stream);
-      if (v == 4) return few_mx4<1, 2, 16, 2, 1>(p, stream);
-      return few_mx4<1, 2, 8, 2, 2>(p, stream);
-    }
-    if (v == 1) return few_mx4<2, 2, 8, 2, 1>(p, stream);
-    if (v == 2) return few_mx4<4, 4, 4, 1, 4, true>(p, stream);
-    if (v == 3) return few_mx4<4, 4, 8, 1, 2, true>(p, stream);
-    if (v == 4) return few_mx4<4, 4, 8, 1, 1>(p, stream);
-    if (v == 5) return few_mx4<2, 4, 4, 1, 4, true>(p, stream);
-    if (v == 6) return few_mx4<2, 4, 8, 1, 2, true>(p, stream);
-    if (v == 7) return few_mx4<2, 2, 4, 1, 4, true>(p, stream);
-    return few_mx4<2, 2, 8, 1, 2>(p, stream);
+    if (p.M > 16) return few_mx4<2, 2, 8, 2, 1>(p, stream);
+    return 4 * rows32 > 3 * cus ? few_mx4<1, 2, 8, 2, 2>(p, stream) : few_mx4<1, 1, 8, 2, 2>(p, stream);
   }
   if (p.M <= 4) {
-    if (v == 1) return few_bf16<1, 1, 1, 16, 2, 2>(p, stream);
-    if (v == 2) return few_bf16<1, 1, 2, 8, 2, 2>(p, stream);
-    if (v == 3) return few_bf16<1, 1, 1, 8, 1, 4>(p, stream);
-    if (v == 4) return few_bf16<1, 1, 1, 16, 1, 4>(p, stream);
-    return few_bf16<1, 1, 1, 8, 2, 2>(p, stream);
+    if (2 * rows16 <= cus) return few_bf16<1, 1, 1, 16, 2, 2>(p, stream);
+    return rows16 > 3 * cus ? few_bf16<1, 1, 2, 8, 2, 2>(p, stream) : few_bf16<1, 1, 1, 8, 2, 2>(p, stream);
   }
-  if (p.M <= 16) {
-    if (v == 1) return few_bf16<1, 4, 2, 8, 1, 3>(p, stream);
-    if (v == 2) return few_bf16<1, 4, 1, 8, 1, 2>(p, stream);
-    if (v == 3) return few_bf16<1, 4, 2, 16, 1, 2>(p, stream);
-    if (v == 4) return few_bf16<1, 4, 4, 8, 1, 1>(p, stream);
-    return few_bf16<1, 4, 2, 8, 1, 2>(p, stream);
-  }
-  if (v == 1) return few_bf16<4, 4, 2, 8, 1, 1>(p, stream);
-  if (v == 2) return few_bf16<2, 4, 2, 8, 1, 1>(p, stream);
-  if (v == 3) return few_bf16<4, 4, 1, 8, 1, 1>(p, stream);
-  if (v == 4) return few_bf16<2, 4, 1, 8, 1, 1>(p, stream);
-  return few_bf16<1, 4, 2, 8, 1, 2>(p, stream);
+  if (p.M > 48 && 2 * rows32 > cus) return few_bf16<4, 4, 2, 8, 1, 1>(p, stream);
+  if (p.M > 16 && rows32 > cus) return few_bf16<2, 4, 2, 8, 1, 1>(p, stream);
+  const int64_t tiles = (p.M + 15) / 16;
+  if (2 * rows16 * tiles <= 3 * cus) return few_bf16<1, 4, 1, 8, 1, 2>(p, stream);
+  return p.M <= 16 && 5 * rows64 > 3 * cus ? few_bf16<1, 4, 4, 8, 1, 1>(p, stream)
+                                           : few_bf16<1, 4, 2, 8, 1, 2>(p, stream);
 }
 
 }  // namespace kda

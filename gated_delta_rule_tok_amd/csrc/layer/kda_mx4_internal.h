@@ -26,8 +26,6 @@ struct Mx4Params {
   int K, N;
 };
 hipError_t launch_mx4_few(const Mx4Params& p, int cus, hipStream_t stream);
-// Operands of k a multiple of 128, 512 at least, and scales at 4-byte addresses.
-bool mx4_tile_ok(const Mx4Params& p);
 hipError_t launch_mx4_tile(const Mx4Params& p, int cus, hipStream_t stream);
 
 // One call of the mixture-of-experts layer.  A pair is a token and an expert that

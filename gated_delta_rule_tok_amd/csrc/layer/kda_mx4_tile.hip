@@ -11,7 +11,6 @@
 // The loads are written in assembly: with the builtin the compiler waits for every
 // load into LDS before each read of it, which leaves one stage in flight.  Their
 // count in flight is waited on by hand.
-#include <cstdlib>
 #include <type_traits>
 
 #include "kda_mx4_dev.h"
@@ -29,10 +28,11 @@ __device__ __forceinline__ void load_lds(i32x4 base, uint32_t voff, uint32_t sof
                :: "s"(lds), "v"(voff), "s"(base), "s"(soff), "i"(more)
                : "memory", "scc");
 }
-__device__ __forceinline__ i32x4 rsrc_of(const void* p) {
+// bytes: behind them loads give zeros
+__device__ __forceinline__ i32x4 rsrc_of(const void* p, uint64_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(p);
-  return i32x4{__builtin_amdgcn_readfirstlane(int(uint32_t(a))), __builtin_amdgcn_readfirstlane(int(a >> 32)), -1,
-               0x00020000};
+  return i32x4{__builtin_amdgcn_readfirstlane(int(uint32_t(a))), __builtin_amdgcn_readfirstlane(int(a >> 32)),
+               __builtin_amdgcn_readfirstlane(int(uint32_t(bytes < 0xffffffffu ? bytes : 0xffffffffu))), 0x00020000};
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)(p)));
@@ -51,8 +51,10 @@ __device__ __forceinline__ void wait_loads() {  // at most N loads under way, an
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(N) : "memory");
 }
 
-// WN: waves along w's rows; two along x's
-template <int BM, int BN, int NS, int WN>
+// WN: waves along w's rows; two along x's.  DIRECT: scales by loads into LDS too, where
+// each row's are at 4-byte addresses, at least 16, and the stages whole; otherwise
+// through registers, whose wait empties the wave's loads once in four stages.
+template <int BM, int BN, int NS, int WN, bool DIRECT>
 __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
   constexpr int kWaves = 2 * WN;
   constexpr int FM = BM / 64, FN = BN / (32 * WN);          // 32 x 32 tiles of a wave, either way
@@ -76,9 +78,11 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
   const int64_t m0 = int64_t(8 * panel + in % width) * BM;
   const int n0 = in / width * BN;
   const uint32_t row_bytes = p.K / 2, nb = p.K / kMxBlock;
-  const i32x4 xb = rsrc_of(static_cast<const uint8_t*>(p.x) + size_t(m0) * row_bytes),
-              wb = rsrc_of(p.w + size_t(n0) * row_bytes), xsb = rsrc_of(p.xs + size_t(m0) * nb),
-              wsb = rsrc_of(p.ws + size_t(n0) * nb);
+  const uint64_t m_left = uint64_t(p.M - m0), n_left = uint64_t(p.N - n0);
+  const uint8_t *xs = p.xs + size_t(m0) * nb, *ws = p.ws + size_t(n0) * nb;
+  const i32x4 xb = rsrc_of(static_cast<const uint8_t*>(p.x) + size_t(m0) * row_bytes, m_left * row_bytes),
+              wb = rsrc_of(p.w + size_t(n0) * row_bytes, n_left * row_bytes),
+              xsb = rsrc_of(xs, m_left * nb), wsb = rsrc_of(ws, n_left * nb);
   const int mlast = int(p.M - 1 - m0 < BM ? p.M - 1 - m0 : BM - 1), nlast = min(p.N - 1 - n0, BN - 1);
   // this lane's source of each load of a stage; rows behind the last repeat it
   uint32_t off[kLoads], soff[kScaleLoads];
@@ -93,7 +97,7 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
     const int r = (wave * kScaleLoads + i) * 64 + lane;
     soff[i] = uint32_t(r < BM ? min(r, mlast) : min(r - BM, nlast)) * nb;
   }
-  const int T = p.K / 128;
+  const int T = (nb + 3) / 4;
   // (a wave's loads are all of x or all of w)
   static_assert(BM == BN, "");
   const i32x4 code_base = wave < kWaves / 2 ? xb : wb, scale_base = wave < kWaves / 2 ? xsb : wsb;
@@ -106,6 +110,25 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
   };
   // The scales of four stages are 16 bytes a row; the last ones of a row are its last
   // 16 bytes, so that no load passes its end.
+  u32x4 held;  // 16 scales of this thread's row, on their way
+  static_assert(BM + BN == 64 * kWaves, "a row each");
+  const auto load_scales = [&](int t) {
+    const int r = threadIdx.x;
+    const uint8_t* at = (r < BM ? xs + size_t(min(r, mlast)) * nb : ws + size_t(min(r - BM, nlast)) * nb) + 4 * t;
+    held = u32x4{};
+    if (4 * t + 16 <= int(nb)) {
+      struct __attribute__((packed, aligned(1))) B { uint32_t v[4]; };
+      const B b = *reinterpret_cast<const B*>(at);
+      held = u32x4{b.v[0], b.v[1], b.v[2], b.v[3]};
+    } else {  // the row's last ones: zeros behind them, so that what is read of its codes there counts nothing
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (4 * t + i < int(nb)) held[i / 4] |= uint32_t(at[i]) << (8 * (i & 3));
+    }
+  };
+  const auto store_scales = [&](int t) {
+    *reinterpret_cast<u32x4*>(L.scale[(t >> 2) & (L.kScales - 1)] + threadIdx.x * 16) = held;
+  };
   const auto issue_scales = [&](int t) {
     if ((t & 3) || t >= T) return;
 #pragma unroll
@@ -133,7 +156,8 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
   };
   const auto read_scale = [&](Scales& o, int t, int i) {
     t = min(t, T - 1);
-    const int at = 4 * t - int(min(uint32_t(4 * (t & ~3)), nb - 16));  // this stage's in the row's 16 bytes
+    // this stage's in the row's 16 bytes
+    const int at = DIRECT ? 4 * t - int(min(uint32_t(4 * (t & ~3)), nb - 16)) : 4 * (t & 3);
     const int r = i < FN ? wr + 32 * i : xr + 32 * (i - FN);
     const uint32_t v = *reinterpret_cast<const uint32_t*>(L.scale[(t >> 2) & (L.kScales - 1)] + at + r * 16);
     if (i < FN)
@@ -158,10 +182,14 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
   };
 #pragma unroll
   for (int t = 0; t < NS; ++t) {
-    issue_scales(t);
+    if (DIRECT) issue_scales(t);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       if (t + 1 < NS || i < kLoads - kLoads / 2) issue(t, i);  // (the rest comes in the loop)
+  }
+  if (!DIRECT) {
+    load_scales(0);
+    store_scales(0);
   }
   wait_loads<(NS - 2) * kLoads>();  // the first stage
   __builtin_amdgcn_s_barrier();
@@ -185,7 +213,13 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
   constexpr int kLate = kLoads / 2;  // of a stage's loads, in the next one's time
   for (int t = 0; t < T; ++t) {
     // (the one branch, in front: the compiler moves MFMAs behind one, all at once)
-    if (t) issue_scales(t + NS - 1);
+    if (DIRECT) {
+      if (t) issue_scales(t + NS - 1);
+    } else if ((t & 3) == 0) {
+      if (t + 4 < T) load_scales(t + 4);
+    } else if ((t & 3) == 3) {
+      if (t + 1 < T) store_scales(t + 1);
+    }
     multiply(f[0], std::integral_constant<int, 0>{}, sc, [&](int n) {
 #pragma unroll
       for (int i = n * kEach; i < (n + 1) * kEach && i < kReads; ++i) read(f[1], t, 1, i);
@@ -254,7 +288,10 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
 
 template <int BM, int BN, int NS, int WN>
 hipError_t launch(const Mx4Params& p, hipStream_t st) {
-  const void* f = reinterpret_cast<const void*>(&tile_kernel<BM, BN, NS, WN>);
+  const auto at = [](const void* q) { return reinterpret_cast<uintptr_t>(q); };
+  const bool direct = p.K % 128 == 0 && p.K >= 512 && at(p.xs) % 4 == 0 && at(p.ws) % 4 == 0;
+  const void* f = direct ? reinterpret_cast<const void*>(&tile_kernel<BM, BN, NS, WN, true>)
+                         : reinterpret_cast<const void*>(&tile_kernel<BM, BN, NS, WN, false>);
   Mx4Params arg = p;
   void* args[] = {&arg};
   const int64_t tiles = ((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
@@ -263,18 +300,10 @@ hipError_t launch(const Mx4Params& p, hipStream_t st) {
 
 }  // namespace
 
-bool mx4_tile_ok(const Mx4Params& p) {
-  return p.K % 128 == 0 && p.K >= 512 && reinterpret_cast<uintptr_t>(p.xs) % 4 == 0 &&
-         reinterpret_cast<uintptr_t>(p.ws) % 4 == 0;
-}
-
 hipError_t launch_mx4_tile(const Mx4Params& p, int cus, hipStream_t stream) {
-  const int64_t big = ((p.M + 255) / 256) * ((p.N + 255) / 256);
-  static const int v = [] { const char* e = getenv("MXT"); return e ? atoi(e) : 0; }();
-  if (v ? v == 2 : 2 * big > cus) return launch<256, 256, 4, 2>(p, stream);
-  if (v == 3) return launch<256, 256, 4, 4>(p, stream);
-  if (v == 4) return launch<128, 128, 8, 1>(p, stream);
-  return launch<128, 128, 8, 2>(p, stream);
+  const int64_t small = ((p.M + 127) / 128) * ((p.N + 127) / 128);
+  if (small <= cus) return launch<128, 128, 8, 2>(p, stream);
+  return launch<256, 256, 4, 4>(p, stream);
 }
 
 }  // namespace kda
