@@ -13,8 +13,6 @@
 // The router in fp64: which experts are chosen does not depend on the order of a
 // sum, and with a whole-number result there is no rounding to hide behind.  It
 // costs 0.75 us of the fp64 matrix pipe per 16 tokens at 256 x 7168.
-#include <type_traits>
-
 #include "kda_mx4_dev.h"
 #include "kda_mx4_internal.h"
 
@@ -25,6 +23,7 @@ typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRouterWaves = 4;
 constexpr int kMaxExperts = 1024;
+constexpr int kWaves = 8;  // of the workgroups of up and down
 
 // v_mfma_f64_16x16x4_f64: lane l holds element (l % 16, k = l / 16) of A and B and
 // rows l / 16 + 4 j of column l % 16 of the result (checked on the device).
@@ -140,135 +139,110 @@ constexpr int kMaxSlots = 64 * 32 + 16 * 16;
 struct RouteLds {
   double key[kMaxExperts], score[kMaxExperts], red[kRouteThreads / 64], chosen[32];
   int chosen_id[32];
+  int16_t best[kMaxExperts / 64 * 32];
 };
 struct ListLds {
   uint64_t mask[kMaxExperts + 16];
   uint16_t first[kMaxExperts + 16], slot_of[kMaxSlots];  // expert * 16 + chunk
+  int16_t ids[64 * 32];
+  float gates[64 * 32];
+  uint64_t live;
+  int total[kRouteThreads / 64];
 };
-__device__ void list_slots(const MoeParams& p, ListLds& L, int16_t* ids) {
-  const int t = threadIdx.x, every = p.E + p.S;
-  __shared__ uint64_t live;
-  __shared__ int slots;
+__device__ void list_slots(const MoeParams& p, ListLds& L) {
+  const int t = threadIdx.x, lane = t & 63, every = p.E + p.S;
   for (int e = t; e < p.E; e += kRouteThreads) L.mask[e] = 0;
-  if (t == 0) live = 0;
+  if (t == 0) L.live = 0;
   __syncthreads();
   const int pairs = p.M * p.top;
   for (int i = t; i < pairs; i += kRouteThreads) {
     const int e = get(p.ids + i);
-    ids[i] = int16_t(e);
+    L.gates[i] = get(p.gates + i);
+    L.ids[i] = int16_t(e);
     if (e >= 0) {
-      atomicOr(reinterpret_cast<unsigned long long*>(&L.mask[e]), 1ull << (i / p.top));
-      if (i % p.top == 0) atomicOr(reinterpret_cast<unsigned long long*>(&live), 1ull << (i / p.top));
+      const int token = i / p.top;
+      atomicOr(reinterpret_cast<unsigned long long*>(&L.mask[e]), 1ull << token);
+      if (i == token * p.top) atomicOr(reinterpret_cast<unsigned long long*>(&L.live), 1ull << token);
     }
   }
   __syncthreads();
-  if (t < p.S) L.mask[p.E + t] = live;
+  if (t < p.S) L.mask[p.E + t] = L.live;
   __syncthreads();
-  if (t < 64) {  // one wave: running numbers of slots and of pairs, 64 experts at a time
-    int slot = 0, begin = 0;
-    const uint64_t below = (1ull << t) - 1;
-    for (int e0 = 0; e0 < every; e0 += 64) {
-      const int e = e0 + t, n = e < every ? __popcll(L.mask[e]) : 0, c = (n + p.chunk - 1) / p.chunk;
-      int at = begin, s = slot;  // what is before this expert, bit by bit of the counts
-      for (int b = 0; (1 << b) <= p.M; ++b) {
-        const uint64_t nb = __ballot((n >> b) & 1), cb = __ballot((c >> b) & 1);
-        at += __popcll(nb & below) << b;
-        begin += __popcll(nb) << b;
-        s += __popcll(cb & below) << b;
-        slot += __popcll(cb) << b;
-      }
-      if (n) L.first[e] = uint16_t(at);
-      for (int i = 0; i < c; ++i) L.slot_of[s + i] = uint16_t(e * 16 + i);
+  // running numbers of slots (upper half) and pairs (lower), an expert a thread
+  int before = 0;
+  for (int e0 = 0; e0 < every; e0 += kRouteThreads) {
+    const int e = e0 + t, n = e < every ? __popcll(L.mask[e]) : 0, c = (n + p.chunk - 1) / p.chunk;
+    int sum = c << 16 | n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(sum, o);
+      if (lane >= o) sum += u;
     }
-    if (t == 0) p.head[1] = slots = slot;
+    if (lane == 63) L.total[t >> 6] = sum;
+    __syncthreads();
+    int at = before + sum - (c << 16 | n);
+#pragma unroll
+    for (int w = 0; w < kRouteThreads / 64; ++w) {
+      if (w < t >> 6) at += L.total[w];
+      before += L.total[w];
+    }
+    __syncthreads();
+    if (n) L.first[e] = uint16_t(at & 0xffff);
+    for (int i = 0; i < c; ++i) L.slot_of[(at >> 16) + i] = uint16_t(e * 16 + i);
   }
+  const int slots = before >> 16, lives = __popcll(L.live);
+  if (t == 0) p.head[1] = slots;
   __syncthreads();
   for (int i = t; i < slots; i += kRouteThreads) {
     const int e = L.slot_of[i] >> 4;
     write_slot(p, i, e, L.mask[e], L.slot_of[i] & 15, L.first[e]);
   }
-  for (int i = t; i < pairs; i += kRouteThreads)
-    if (ids[i] >= 0)
-      p.pair_gate[L.first[ids[i]] + __popcll(L.mask[ids[i]] & ((1ull << (i / p.top)) - 1))] = get(p.gates + i);
-  for (int i = t; i < p.S * __popcll(live); i += kRouteThreads) p.pair_gate[__popcll(live) * p.top + i] = 1.f;
-}
-
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  const auto step = [](uint32_t v, auto ctrl) {
-    return max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), decltype(ctrl)::value, 0xf, 0xf, false)));
-  };
-  v = step(v, std::integral_constant<int, 0x111>{});  // from 1, 2, 4, 8 lanes below in a row of 16
-  v = step(v, std::integral_constant<int, 0x112>{});
-  v = step(v, std::integral_constant<int, 0x114>{});
-  v = step(v, std::integral_constant<int, 0x118>{});
-  v = step(v, std::integral_constant<int, 0x142>{});  // a row's last lane to the next row
-  v = step(v, std::integral_constant<int, 0x143>{});  // the second row's to the upper half
-  return uint32_t(__builtin_amdgcn_readlane(int(v), 63));
-}
-
-// The top largest keys, one wave: the largest of 64-bit numbers that order as the keys,
-// top times, the upper 32 bits first and, where several have them, the lower.
-template <int kSlots>
-__device__ __forceinline__ void choose(const MoeParams& p, const double* key, const double* score, double* chosen,
-                                       int* chosen_id, int m) {
-  const int t = threadIdx.x;
-  uint32_t hi[kSlots], lo[kSlots];
-#pragma unroll
-  for (int s = 0; s < kSlots; ++s) {
-    hi[s] = lo[s] = 0;  // below every key
-    if (64 * s + t < p.E) {
-      const uint64_t b = __builtin_bit_cast(uint64_t, key[64 * s + t] + 0.0);  // (-0 is 0)
-      const uint64_t o = b >> 63 ? ~b : b | 1ull << 63;
-      hi[s] = uint32_t(o >> 32), lo[s] = uint32_t(o);
-    }
+  for (int i = t; i < pairs; i += kRouteThreads) {
+    const int e = L.ids[i];
+    if (e >= 0) p.pair_gate[L.first[e] + __popcll(L.mask[e] & ((1ull << (i / p.top)) - 1))] = L.gates[i];
   }
-  int left = min(p.top, p.E);
-  for (int j = 0; j < left; ++j) {
-    uint32_t v = 0;
-#pragma unroll
-    for (int s = 0; s < kSlots; ++s)
-      v = max(v, hi[s]);
-    v = wave_max(v);
-    uint32_t w = 0;
-    int several = 0;
-#pragma unroll
-    for (int s = 0; s < kSlots; ++s)
-      several += __popcll(__ballot(hi[s] == v));
-    if (several > 1) {
-#pragma unroll
-      for (int s = 0; s < kSlots; ++s)
-        if (hi[s] == v) w = max(w, lo[s]);
-      w = wave_max(w);
+  for (int i = t; i < p.S * lives; i += kRouteThreads) p.pair_gate[lives * p.top + i] = 1.f;
+}
+
+// The top largest keys, of equal ones the first: each wave ranks 64 adjacent experts at a
+// time, then the best of those are ranked among each other.
+__device__ __forceinline__ void choose(const MoeParams& p, RouteLds& L, int m) {
+  const int t = threadIdx.x, lane = t & 63;
+  for (int e0 = t & ~63; e0 < p.E; e0 += kRouteThreads) {
+    const int e = e0 + lane, end = min(64, p.E - e0);
+    const double v = L.key[min(e, p.E - 1)];
+    int rank = 0;
+#pragma unroll 8
+    for (int i = 0; i < end; ++i) {
+      const double o = L.key[e0 + i];
+      rank += o > v || (o == v && i < lane) ? 1 : 0;
     }
-    int e = -1;
-#pragma unroll
-    for (int s = 0; s < kSlots; ++s) {
-      if (e < 0) {
-        const uint64_t at = __ballot(hi[s] == v && (several == 1 || lo[s] == w));
-        if (at) {
-          e = 64 * s + __builtin_ctzll(at);
-          if (64 * s + t == e) hi[s] = lo[s] = 0;
-        }
-      }
+    if (lane < end && rank < p.top) L.best[(e0 >> 6) * p.top + rank] = int16_t(e);
+  }
+  __syncthreads();
+  const int whole = (p.E - 1) >> 6, n = whole * p.top + min(p.top, p.E - 64 * whole);
+  for (int i = t; i < n; i += kRouteThreads) {
+    const int e = L.best[i];
+    const double v = L.key[e];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const int f = L.best[j];
+      const double o = L.key[f];
+      rank += o > v || (o == v && f < e) ? 1 : 0;
     }
-    if (t == 0) {
-      chosen[j] = score[e];
-      chosen_id[j] = e;
-      put(p.ids + m * p.top + j, e);
+    if (rank < p.top) {
+      L.chosen[rank] = L.score[e];
+      L.chosen_id[rank] = e;
+      put(p.ids + m * p.top + rank, e);
     }
   }
 }
 
-// SLOTS: experts / 64 at most (short code: a launch of one workgroup per token runs from
-// a cold instruction cache)
-template <int SLOTS>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeParams p) {
   __shared__ union {
     RouteLds route;
-    struct {
-      ListLds list;
-      int16_t ids[64 * 32];
-    };
+    ListLds list;
   } L;
   double *key = L.route.key, *score = L.route.score, *red = L.route.red, *chosen = L.route.chosen;
   int* chosen_id = L.route.chosen_id;
@@ -312,7 +286,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeParams p) {
       key[e] = v == v ? v : -INFINITY;
     }
     __syncthreads();
-    if (t < 64) choose<SLOTS>(p, key, score, chosen, chosen_id, m);
+    choose(p, L.route, m);
     __syncthreads();
     if (t < p.top) {
       double sum = 1;
@@ -334,7 +308,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeParams p) {
     if (t == 0) p.head[1] = n;
     return;
   }
-  if (come_last(p.head, p.M)) list_slots(p, L.list, L.ids);
+  if (come_last(p.head, p.M)) list_slots(p, L.list);
 }
 
 // Data that a launch before this one wrote, read through the scalar cache.
@@ -361,18 +335,14 @@ struct SlotView {
   }
 };
 
-constexpr int kUpWaves = 8;
-
 // A workgroup's items are adjacent (slot, tile of 16 rows) pairs; the units of k of a
 // wave, item after item, go through a ring of U, so that the next item's loads are
 // under way while this one is joined.
 template <int RQ, int STEPS, int U, bool TINY>
-__global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(4, 4))) void up_kernel(MoeParams p) {
-  // two halves in turn where they fit beside two workgroups' operands
-  constexpr int kHalves = RQ == 1 ? 2 : 1;
+__global__ __launch_bounds__(64 * kWaves, 4) void up_kernel(MoeParams p) {
   constexpr int kX = STEPS * RQ * 1024, kWave = kX + 2 * kPieceLds<STEPS>;
-  __shared__ __align__(16) char lds[kUpWaves * kWave];
-  __shared__ f32x4 red[kHalves][kUpWaves][2][64];
+  __shared__ __align__(16) char lds[kWaves * kWave];
+  __shared__ f32x4 red[kWaves][2][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int tiles = p.I / 16;
@@ -380,7 +350,7 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(4
   const uint32_t lo = items * blockIdx.x >> p.up_log2, hi = items * (blockIdx.x + 1) >> p.up_log2;
   if (lo >= hi) return;
   const int nb = p.K / kMxBlock, units = (nb + 4 * STEPS - 1) / (4 * STEPS);
-  const int first = units * wave / kUpWaves, cnt = units * (wave + 1) / kUpWaves - first;
+  const int first = units * wave / kWaves, cnt = units * (wave + 1) / kWaves - first;
   char *xl = lds + wave * kWave, *wl = xl + kX;
   const uint32_t row_bytes = p.K / 2, code_row = (lane >> 2) * row_bytes, scale_row = (lane >> 2) * nb;
   const int slot0 = lo / tiles, tile0 = lo - slot0 * tiles;
@@ -389,11 +359,12 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(4
     Piece<STEPS> w[2];
     XRows<RQ> x[STEPS];
   } buf[U];
-  // what is loaded next
-  int left_items = hi - lo, slot = slot0, tile = tile0, unit = 0;
+  // what is loaded next; n of the slot that is loaded and of the one that is used
+  int n_load = 0, n_use = 0, left_items = hi - lo, slot = slot0, tile = tile0, unit = 0;
   const uint8_t *codes[2], *scales[2];
   uint32_t row[RQ];
   const auto aim_slot = [&](const SlotView& s) {
+    n_load = s.n;
     const uint32_t x_bytes = uint32_t(p.x_row) * 2;
     row[0] = s.token4<0>(g) * x_bytes;
     if (RQ > 1) {
@@ -418,7 +389,7 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(4
     for (int i = 0; i < 2; ++i)
       load_piece<STEPS, TINY>(b.w[i], codes[i], code_row, scales[i], scale_row, nb, first + unit, lane & 3);
 #pragma unroll
-    for (int j = 0; j < STEPS; ++j) load_x<RQ>(b.x[j], p.x, row, ((first + unit) * STEPS + j) * 128, p.K, l16);
+    for (int j = 0; j < STEPS; ++j) load_x<RQ>(b.x[j], p.x, row, ((first + unit) * STEPS + j) * 128, p.K, l16, n_load);
     if (++unit == cnt) {
       unit = 0;
       if (--left_items > 0) {
@@ -435,7 +406,7 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(4
     for (int i = 0; i < 2; ++i) stage_piece<STEPS, TINY>(wl + i * kPieceLds<STEPS>, b.w[i], nb, first + unit, lane);
 #pragma unroll
     for (int j = 0; j < STEPS; ++j)
-      stage_x<RQ>(xl + j * (RQ * 1024), b.x[j], ((first + unit) * STEPS + j) * 128, p.K, l16, g);
+      stage_x<RQ>(xl + j * (RQ * 1024), b.x[j], ((first + unit) * STEPS + j) * 128, p.K, l16, g, n_use);
     wave_lds_fence();
 #pragma unroll
     for (int j = 0; j < STEPS; ++j) {
@@ -453,15 +424,12 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(4
     }
     wave_lds_fence();
   };
-  // joins the waves' sums of an item (of two halves, the other one is free once all have come)
-  int at_slot = slot0, at_tile = tile0, half = 0;
+  int items_left = hi - lo;
+  // joins the waves' sums of an item
+  int at_slot = slot0, at_tile = tile0;
   const auto join = [&]() {
-    auto& r = red[half];
-    if (kHalves == 2)
-      half ^= 1;
-    else
-      __syncthreads();
-    r[wave][0][lane] = acc[0], r[wave][1][lane] = acc[1];
+    __syncthreads();  // the last item's are read
+    red[wave][0][lane] = acc[0], red[wave][1][lane] = acc[1];
     acc[0] = acc[1] = f32x4{};
     __syncthreads();
     if (wave < RQ) {
@@ -471,10 +439,10 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(4
         const auto* gate4 = scalar(p.pair_gate) + s.begin + 4 * wave;
         const float g0 = gate4[0], g1 = gate4[1], g2 = gate4[2], g3 = gate4[3];
         const float gate = g & 2 ? (g & 1 ? g3 : g2) : (g & 1 ? g1 : g0);
-        const float* at = reinterpret_cast<const float*>(&r[0][0][(n >> 2) * 16 + m]) + (n & 3);
+        const float* at = reinterpret_cast<const float*>(&red[0][0][(n >> 2) * 16 + m]) + (n & 3);
         float a = at[0], u = at[256];
 #pragma unroll
-        for (int w = 1; w < kUpWaves; ++w) a += at[w * 512], u += at[w * 512 + 256];
+        for (int w = 1; w < kWaves; ++w) a += at[w * 512], u += at[w * 512 + 256];
         if (m < s.n) {
           const float h = a / (1.f + __expf(-a)) * u * gate;
           const uint16_t top = f32_to_bf16(h);
@@ -484,9 +452,11 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(4
         }
       }
     }
-    if (++at_tile == tiles) at_tile = 0, ++at_slot;
+    if (++at_tile == tiles) {
+      at_tile = 0, ++at_slot;
+      if (items_left > 1) n_use = scalar(p.slot + at_slot)->n;
+    }
   };
-  int items_left = hi - lo;
   if (cnt == 0) {  // (fewer units than waves)
     for (; items_left > 0; --items_left) join();
     return;
@@ -495,6 +465,7 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(4
     const SlotView s(p.slot + slot0);
     aim_slot(s);
     aim_tile(s.expert);
+    n_use = s.n;
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) load(buf[u]);
@@ -513,10 +484,8 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(4
   }
 }
 
-constexpr int kDownWaves = 8;
-
 template <int RQ, int U, bool TINY>
-__global__ __launch_bounds__(64 * kDownWaves, 4) void down_kernel(MoeParams p) {
+__global__ __launch_bounds__(64 * kWaves, 4) void down_kernel(MoeParams p) {
   extern __shared__ __align__(16) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
@@ -524,12 +493,12 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void down_kernel(MoeParams p) {
   const int nb = p.I / kMxBlock, units = (nb + 3) / 4;
   const uint32_t jobs = scalar(p.head)[1] * units;
   // this wave's run of (slot, unit of k)
-  const uint32_t share = part * kDownWaves + wave, shares = p.parts * kDownWaves;
+  const uint32_t share = part * kWaves + wave, shares = p.parts * kWaves;
   const int first = jobs * share / shares, end = jobs * (share + 1) / shares;
   constexpr int kWave = RQ * 1024 + kPieceLds<1>;
   char *hl = lds + wave * kWave, *wl = hl + RQ * 1024;
   // [wave][token][16]: this wave's sums
-  f32x4* y = reinterpret_cast<f32x4*>(lds + kDownWaves * kWave) + wave * p.M * 4;
+  f32x4* y = reinterpret_cast<f32x4*>(lds + kWaves * kWave) + wave * p.M * 4;
   for (int i = lane; i < p.M * 4; i += 64) y[i] = f32x4{};
   wave_lds_fence();
   if (first < end) {
@@ -544,8 +513,10 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void down_kernel(MoeParams p) {
     const uint8_t *codes, *scales;
     const uint16_t *hi, *lo;
     uint32_t row[RQ];
+    int n_load = 0, n_use = 0;  // of the slot that is loaded and of the one that is used
     const auto aim = [&]() {
       const SlotView s(p.slot + slot);
+      n_load = s.n;
       const size_t r = size_t(s.expert) * p.K + n0, at = size_t(s.begin) * p.I;
       codes = p.w_down + r * row_bytes;
       scales = p.s_down + r * nb;
@@ -556,8 +527,8 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void down_kernel(MoeParams p) {
     const auto load = [&](Unit& b) {
       if (job == end) return;
       load_piece<1, TINY>(b.w, codes, code_row, scales, scale_row, nb, unit, lane & 3);
-      load_x<RQ>(b.hi, hi, row, unit * 128, p.I, l16);
-      load_x<RQ>(b.lo, lo, row, unit * 128, p.I, l16);
+      load_x<RQ>(b.hi, hi, row, unit * 128, p.I, l16, n_load);
+      load_x<RQ>(b.lo, lo, row, unit * 128, p.I, l16, n_load);
       if (++job < end && ++unit == units) {
         unit = 0;
         ++slot;
@@ -567,7 +538,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void down_kernel(MoeParams p) {
     f32x4 acc = {};
     const auto use = [&](Unit& b, int unit) {
       stage_piece<1, TINY>(wl, b.w, nb, unit, lane);
-      stage_x<RQ>(hl, b.hi, unit * 128, p.I, l16, g);
+      stage_x<RQ>(hl, b.hi, unit * 128, p.I, l16, g, n_use);
       wave_lds_fence();
       const float sc = scale_of(scale_operand<1>(wl, 0, l16, g));
       const u32x4 c = codes_operand(wl, 0, l16, g);
@@ -577,7 +548,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void down_kernel(MoeParams p) {
 #pragma unroll
       for (int d = 0; d < 4; ++d) acc = mfma32(w[d], x_operand<RQ>(hl, d, l16, g), acc);
       wave_lds_fence();
-      stage_x<RQ>(hl, b.lo, unit * 128, p.I, l16, g);
+      stage_x<RQ>(hl, b.lo, unit * 128, p.I, l16, g, n_use);
       wave_lds_fence();
 #pragma unroll
       for (int d = 0; d < 4; ++d) acc = mfma32(w[d], x_operand<RQ>(hl, d, l16, g), acc);
@@ -595,9 +566,11 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void down_kernel(MoeParams p) {
         acc = f32x4{};
         ++at_slot;
         at_unit = 0;
+        if (at < end) n_use = scalar(p.slot + at_slot)->n;
       }
     };
     aim();
+    n_use = n_load;
 #pragma unroll
     for (int u = 0; u < U; ++u) load(buf[u]);
     for (bool more = true; more;) {
@@ -610,18 +583,18 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void down_kernel(MoeParams p) {
     }
   }
   __syncthreads();
-  const float* all = reinterpret_cast<const float*>(lds + kDownWaves * kWave);
+  const float* all = reinterpret_cast<const float*>(lds + kWaves * kWave);
   if (p.parts > 1) {
     // a part's sums to the workspace; who comes last adds them up, in their order
-    for (int i = threadIdx.x; i < p.M * 16; i += 64 * kDownWaves) {
+    for (int i = threadIdx.x; i < p.M * 16; i += 64 * kWaves) {
       float s = all[i];
 #pragma unroll
-      for (int w = 1; w < kDownWaves; ++w) s += all[w * p.M * 16 + i];
+      for (int w = 1; w < kWaves; ++w) s += all[w * p.M * 16 + i];
       put(p.sums + (size_t(part) * p.M + (i >> 4)) * p.K + n0 + (i & 15), s);
     }
     if (!come_last(p.done + blockIdx.x, p.parts)) return;
   }
-  for (int i = threadIdx.x; i < p.M * 16; i += 64 * kDownWaves) {
+  for (int i = threadIdx.x; i < p.M * 16; i += 64 * kWaves) {
     const int m = i >> 4;
     if (p.idx && p.idx[m] < 0) continue;
     float s = 0.f;
@@ -629,7 +602,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void down_kernel(MoeParams p) {
       for (int q = 0; q < p.parts; ++q) s += get(p.sums + (size_t(q) * p.M + m) * p.K + n0 + (i & 15));
     } else {
 #pragma unroll
-      for (int w = 0; w < kDownWaves; ++w) s += all[w * p.M * 16 + i];
+      for (int w = 0; w < kWaves; ++w) s += all[w * p.M * 16 + i];
     }
     p.out[m * p.out_row + n0 + (i & 15)] = f32_to_bf16(s);
   }
@@ -647,8 +620,8 @@ int moe_slots(int M, int E, int S, int top, int chunk) {
 // Parts of down's sum over slots: two workgroups per compute unit of 256, while a part
 // has a unit of k for each of its waves.
 int moe_parts(int M, int K, int I, int E, int S, int top, int chunk) {
-  const int tiles = K / 16, units = (I + 255) / 256;
-  const int64_t shares = int64_t(moe_slots(M, E, S, top, chunk)) * units / kDownWaves;
+  const int tiles = K / 16, units = (I + 127) / 128;
+  const int64_t shares = int64_t(moe_slots(M, E, S, top, chunk)) * units / kWaves;
   int parts = 512 / tiles;
   if (parts > shares) parts = int(shares);
   if (parts > kMoeMostParts) parts = kMoeMostParts;
@@ -688,9 +661,12 @@ MoeLayout moe_layout(int M, int K, int I, int E, int S, int top) {
 
 hipError_t launch_moe(const MoeParams& params, int cus, hipStream_t st) {
   MoeParams p = params;
-  // Tokens per slot: 4 where an expert that is hit has about two.  Those with more are
-  // read once for each 4 (from the L2, by workgroups that run at the same time).
-  p.chunk = p.M <= 4 || p.M * p.top <= 2 * p.E ? 4 : 16;
+  // Tokens per slot.  4, with two units of k in flight, where an expert that is hit has
+  // about one: us with 4 / 16, 7168 x 512 x 256 experts, 8 + 1 of them a token: 16 tokens
+  // 126 / 152, 64 tokens 288 / 279; 2048 x 1024 x 128 experts, 8 a token: 16 tokens 68 / 72,
+  // 32 tokens 94 / 91; 8 experts, 64 tokens 46 / 36.  What has more tokens than a slot is read
+  // once for each slot, from the L2 mostly: by workgroups that run at the same time.
+  p.chunk = p.M <= 4 || p.M * p.top <= p.E ? 4 : 16;
   p.parts = moe_parts(p.M, p.K, p.I, p.E, p.S, p.top, p.chunk);
   void* args[] = {&p};
   const auto go = [&](auto* f, dim3 grid, int threads, size_t lds) {
@@ -698,25 +674,27 @@ hipError_t launch_moe(const MoeParams& params, int cus, hipStream_t st) {
   };
   hipError_t e = go(&logits_kernel, dim3((p.E + 15) / 16, p.slices, (p.M + 15) / 16), 64 * kRouterWaves, 0);
   if (e != hipSuccess) return e;
-  e = go(p.E <= 256 ? &route_kernel<4> : &route_kernel<kMaxExperts / 64>, dim3(p.M), kRouteThreads, 0);
+  e = go(&route_kernel, dim3(p.M), kRouteThreads, 0);
   if (e != hipSuccess) return e;
   // a power of two of workgroups, about two per compute unit
   const int64_t items = int64_t(moe_slots(p.M, p.E, p.S, p.top, p.chunk)) * (p.I / 16);
   p.up_log2 = 0;
   while ((int64_t(1) << p.up_log2) < items && (2 << p.up_log2) <= 2 * cus) ++p.up_log2;
-  const dim3 up(1u << p.up_log2);
-  const size_t sums = size_t(kDownWaves) * p.M * 64;
-  const dim3 down(p.K / 16, p.parts);
+  const dim3 up(1u << p.up_log2), down(p.K / 16, p.parts);
+  const size_t sums = size_t(kWaves) * p.M * 64;
+  // With 16 tokens a slot one unit of k in flight leaves registers for another workgroup:
+  // 64 x 2080 x 1056, 40 experts 79 us against 85 with two, 64 x 7168 x 512, 256 experts
+  // 273 against 286.
   if (p.chunk == 4) {
-    e = go(p.K < 128 ? &up_kernel<1, 2, 2, true> : &up_kernel<1, 2, 2, false>, up, 64 * kUpWaves, 0);
+    e = go(p.K < 128 ? &up_kernel<1, 2, 2, true> : &up_kernel<1, 2, 2, false>, up, 64 * kWaves, 0);
     if (e != hipSuccess) return e;
-    return go(p.I < 128 ? &down_kernel<1, 4, true> : &down_kernel<1, 4, false>, down, 64 * kDownWaves,
-              sums + kDownWaves * (1024 + kPieceLds<1>));
+    return go(p.I < 128 ? &down_kernel<1, 4, true> : &down_kernel<1, 4, false>, down, 64 * kWaves,
+              sums + kWaves * (1024 + kPieceLds<1>));
   }
-  e = go(p.K < 128 ? &up_kernel<4, 1, 2, true> : &up_kernel<4, 1, 2, false>, up, 64 * kUpWaves, 0);
+  e = go(p.K < 128 ? &up_kernel<4, 1, 1, true> : &up_kernel<4, 1, 1, false>, up, 64 * kWaves, 0);
   if (e != hipSuccess) return e;
-  return go(p.I < 128 ? &down_kernel<4, 2, true> : &down_kernel<4, 2, false>, down, 64 * kDownWaves,
-            sums + kDownWaves * (4096 + kPieceLds<1>));
+  return go(p.I < 128 ? &down_kernel<4, 1, true> : &down_kernel<4, 1, false>, down, 64 * kWaves,
+            sums + kWaves * (4096 + kPieceLds<1>));
 }
 
 }  // namespace kda

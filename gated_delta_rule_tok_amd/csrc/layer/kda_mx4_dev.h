@@ -116,20 +116,22 @@ template <int RQ>
 struct XRows {
   u32x4 v[RQ];
 };
-// x: a scalar; row[q]: bytes from there to row 4 q + lane / 16; K: elements of a row.
+// x: a scalar; row[q]: bytes from there to row 4 q + lane / 16; K: elements of a row;
+// n: rows that are wanted (what the others' columns give is not used).
 template <int RQ>
 __device__ __forceinline__ void load_x(XRows<RQ>& x, const uint16_t* base, const uint32_t (&row)[RQ], int k0, int K,
-                                       int l16) {
+                                       int l16, int n = 4 * RQ) {
   k0 = min(k0, K - 8);
   const uint16_t* at = base + k0;
   const int rest = (K - 8 - k0) >> 3;
 #pragma unroll
   for (int q = 0; q < RQ; ++q)
-    x.v[q] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(at) + (row[q] + uint32_t(min(l16, rest)) * 16));
+    if (4 * q < n)
+      x.v[q] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(at) + (row[q] + uint32_t(min(l16, rest)) * 16));
 }
 // Pieces behind the end of k (they repeat another) as zeros.
 template <int RQ>
-__device__ __forceinline__ void stage_x(char* lds, XRows<RQ>& x, int k0, int K, int l16, int g) {
+__device__ __forceinline__ void stage_x(char* lds, XRows<RQ>& x, int k0, int K, int l16, int g, int n = 4 * RQ) {
   if (k0 + 128 > K) {
     const bool in = k0 + 8 * l16 < K;
 #pragma unroll
@@ -139,7 +141,7 @@ __device__ __forceinline__ void stage_x(char* lds, XRows<RQ>& x, int k0, int K, 
 #pragma unroll
   for (int q = 0; q < RQ; ++q) {
     const int r = 4 * q + g;
-    *reinterpret_cast<u32x4*>(lds + r * 256 + ((l16 ^ r) << 4)) = x.v[q];
+    if (4 * q < n) *reinterpret_cast<u32x4*>(lds + r * 256 + ((l16 ^ r) << 4)) = x.v[q];
   }
 }
 // (rows that are not staged repeat those that are: their columns are not used)

@@ -60,7 +60,7 @@ __device__ __forceinline__ void ring(Unit (&buf)[U], int first, int end, const L
 // NT tiles of 16 tokens (the first 4 RQ rows of each hold tokens), RT tiles of 16 rows of
 // w; U units of STEPS * 128 k in flight.
 template <int NT, int RQ, int RT, int WAVES, int STEPS, int U, bool TINY>
-__global__ __launch_bounds__(64 * WAVES, NT > 2 ? 2 : 4) void few_bf16_kernel(Mx4Params p) {
+__global__ __launch_bounds__(64 * WAVES, NT > 1 ? 2 : 4) void few_bf16_kernel(Mx4Params p) {
   constexpr int kX = STEPS * NT * RQ * 1024, kWave = kX + RT * kPieceLds<STEPS>;
   __shared__ __align__(16) char lds[WAVES * (kWave > NT * RT * 1024 ? kWave : NT * RT * 1024)];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

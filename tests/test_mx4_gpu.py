@@ -199,6 +199,81 @@ def test_proj_of_codes(m, k, n):
     assert torch.equal(y, y2)
 
 
+# tiles through LDS: one and several stages of 128, the last in part, scales of 512 in part,
+# rows and columns of tiles in part, more tiles than compute units
+TILES = [(1024, 32, 1030), (1100, 96, 1000), (1024, 128, 1024), (1025, 160, 1030), (2000, 256, 600), (1030, 416, 1024),
+         (1024, 480, 1030), (1024, 512, 1024), (1030, 640, 1100), (129, 896, 8200), (8200, 1152, 130),
+         (1024, 2080, 1100), (4500, 544, 4400), (4300, 1024, 4400), (70, 2048, 15000), (5000, 64, 5000)]
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("m,k,n", TILES)
+def test_proj_in_tiles(m, k, n, shift):
+    """shift: the scales begin at an odd address."""
+    import torch
+    x, xs = _weights((m,), k, m + k, spread=3)
+    w, ws = _weights((n,), k, n)
+    if shift:
+        def moved(t):
+            flat = torch.full((t.numel() + 1,), 0xAA, dtype=torch.uint8, device="cuda")
+            flat[1:] = t.flatten()
+            return flat[1:].view(t.shape)
+        xs, ws = moved(xs), moved(ws)
+    y = torch.full((m + 1, n + 3), 3.0, dtype=torch.bfloat16, device="cuda")
+    _kda().kda_mx4_proj(x, xs, w, ws, y[:m, :n])
+    _check_product(_values(x, xs), w, ws, y[:m, :n], f"tiles {m}x{k}x{n}")
+    assert (y[m:] == 3).all() and (y[:, n:] == 3).all()
+    y2 = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    _kda().kda_mx4_proj(x, xs, w, ws, y2)
+    assert torch.equal(y[:m, :n], y2)
+
+
+def test_proj_in_tiles_rows_do_not_mix():
+    """NaN scales of one token and of one weight row stay in their row and column, also in
+    the last blocks of k."""
+    import torch
+    m, k, n = 1100, 544, 1000
+    x, xs = _weights((m,), k, 20)
+    w, ws = _weights((n,), k, 21)
+    y, z = (torch.empty(m, n, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    _kda().kda_mx4_proj(x, xs, w, ws, y)
+    xs[1099, 16] = 255
+    ws[500, 0] = 255
+    _kda().kda_mx4_proj(x, xs, w, ws, z)
+    hit = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+    hit[1099] = hit[:, 500] = True
+    assert z[hit].isnan().all() and torch.equal(z[~hit], y[~hit])
+
+
+def test_operands_of_more_than_4_gib():
+    """Rows whose offsets pass 32 bits."""
+    import torch
+    k, n = 65536, 140000
+    w = torch.randint(0, 256, (n, k // 2), generator=_gen(22), device="cuda", dtype=torch.uint8)
+    ws = torch.randint(100, 140, (n, k // 32), generator=_gen(23), device="cuda", dtype=torch.uint8)
+    assert w.numel() > 1 << 32
+    y = torch.full((3, n), math.nan, dtype=torch.bfloat16, device="cuda")
+    x, xs = _weights((3,), k, 24)
+    at = torch.cat((torch.arange(20), torch.arange(n - 40, n))).cuda()
+    _kda().kda_mx4_proj(x, xs, w, ws, y)
+    _check_product(_values(x, xs), w[at], ws[at], y[:, at], "codes, large w")
+    b = torch.randn(3, k, generator=_gen(25), device="cuda").bfloat16()
+    _kda().kda_mx4_proj(b, None, w, ws, y)
+    _check_product(b.double(), w[at], ws[at], y[:, at], "bf16, large w")
+    # as the rows of x in tiles, against few rows of w
+    z = torch.full((n, 70), math.nan, dtype=torch.bfloat16, device="cuda")
+    few, few_s = _weights((70,), k, 26)
+    _kda().kda_mx4_proj(w, ws, few, few_s, z)
+    _check_product(_values(w[at], ws[at]), few, few_s, z[at], "tiles, large x")
+    del y, z
+    v = torch.empty(n, k, dtype=torch.bfloat16, device="cuda")
+    _kda().kda_mx4_dequant(w, ws, v)
+    assert torch.equal(v[at].double(), _values(w[at], ws[at]))
+    c, s = _run_quant(v)
+    rc, rs = _quant(v[at])
+    assert torch.equal(c[at], rc) and torch.equal(s[at], rs)
+
+
 @pytest.mark.parametrize("m", [3, 20, 150])
 def test_proj_of_strided_rows(m):
     import torch
@@ -357,6 +432,8 @@ MOE = [
     (16, 256, 128, 8, 2, 0, False), (17, 288, 64, 4, 4, 1, True), (33, 128, 96, 256, 8, 1, True),
     (64, 512, 256, 64, 8, 1, False), (64, 96, 32, 2, 1, 0, True), (64, 64, 64, 1000, 32, 16, False),
     (21, 2080, 1056, 40, 4, 0, False), (64, 1056, 352, 3, 2, 2, False), (1, 64, 64, 1024, 32, 0, True),
+    (64, 288, 160, 300, 5, 1, True), (48, 4128, 32, 20, 3, 0, False), (5, 32, 2080, 9, 9, 0, True),
+    (30, 96, 4096, 6, 1, 16, False), (64, 512, 64, 600, 9, 0, False),
 ]
 
 
@@ -393,6 +470,23 @@ def test_moe_of_padding_rows(m, pads):
     assert (p.out[pads] == 9).all() and (p.ids[pads] == -1).all() and (p.gates[pads] == 0).all()
     if live:
         p.check("padding", live)
+
+
+def test_moe_of_one_expert_for_all():
+    """Every token to the same experts; and to experts of its own."""
+    import torch
+    for m in (4, 17, 64):
+        p = Moe(m, 128, 64, 64, 1, 0, False, seed=38)
+        p.x[:] = p.x[0]
+        p.run().check("all to one")
+        p = Moe(m, 128, 64, 64, 1, 0, True, seed=39)
+        p.router.zero_()
+        p.router[:, :64] = torch.eye(64, device="cuda").bfloat16()
+        p.x.zero_()
+        p.x[torch.arange(m), torch.arange(m)] = 9
+        p.x[:, 64:] = torch.randn(m, 64, generator=_gen(40), device="cuda").bfloat16()
+        p.run().check("each its own")
+        assert torch.equal(p.ids[:, 0].cpu(), torch.arange(m, dtype=torch.int32))
 
 
 def test_moe_of_equal_scores():
