@@ -751,14 +751,6 @@ def kda_w4_proj(x, w, scales, zeros, y, group_size: int, stream=None) -> None:
 
 # ---- include/kda_mx4.h: microscaled 4-bit numbers ------------------------------
 
-def _mx4(codes, scales, names, shape, index):
-    """Device pointers of dense codes [..., k / 2] and scales [..., k / 32] of `shape` [..., k]."""
-    torch = _torch_module
-    *rows, k = shape
-    return (_on(codes, names[0], torch.uint8, (*rows, k // 2), index),
-            _on(scales, names[1], torch.uint8, (*rows, k // 32), index))
-
-
 def _columns(k, name):
     if k % 32 or k <= 0:
         raise ValueError(f"{name} must have a multiple of 32 columns, got {k}")
@@ -777,8 +769,9 @@ def kda_mx4_quant(x, codes, scales, stream=None) -> None:
         raise ValueError(f"x must be [M, k], got {tuple(x.shape)}")
     m, k = shape = x.shape
     _columns(k, "x")
-    ptrs = (_view(x, "x", _torch_module.bfloat16, shape, dev),
-            *_mx4(codes, scales, ("codes", "scales"), shape, dev))
+    u8 = _torch_module.uint8
+    ptrs = (_view(x, "x", _torch_module.bfloat16, shape, dev), _on(codes, "codes", u8, (m, k // 2), dev),
+            _on(scales, "scales", u8, (m, k // 32), dev))
     _call("kda_mx4_quant", lib.kda_mx4_quant, dev, stream, ptrs, (m, k, _row_stride(x, "x")))
 
 
@@ -791,7 +784,8 @@ def kda_mx4_dequant(codes, scales, out, stream=None) -> None:
         raise ValueError(f"out must be [M, k], got {tuple(out.shape)}")
     m, k = shape = out.shape
     _columns(k, "out")
-    ptrs = (*_mx4(codes, scales, ("codes", "scales"), shape, dev),
+    u8 = _torch_module.uint8
+    ptrs = (_on(codes, "codes", u8, (m, k // 2), dev), _on(scales, "scales", u8, (m, k // 32), dev),
             _view(out, "out", _torch_module.bfloat16, shape, dev))
     _call("kda_mx4_dequant", lib.kda_mx4_dequant, dev, stream, ptrs, (m, k, _row_stride(out, "out")))
 
@@ -810,15 +804,15 @@ def kda_mx4_proj(x, x_scales, w, w_scales, y, stream=None) -> None:
     if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("x and w must be 2-D tensors")
     m, k = x.shape
-    n = w.shape[0]
+    n, u8 = w.shape[0], torch.uint8
     if x_scales is None:
         _columns(k, "x")
         xp, xs, row = _view(x, "x", torch.bfloat16, (m, k), dev), None, _row_stride(x, "x")
     else:
         k *= 2
         _columns(k, "x (of values)")
-        (xp, xs), row = _mx4(x, x_scales, ("x", "x_scales"), (m, k), dev), 0
-    ptrs = (xp, xs, *_mx4(w, w_scales, ("w", "w_scales"), (n, k), dev),
+        xp, xs, row = _on(x, "x", u8, (m, k // 2), dev), _on(x_scales, "x_scales", u8, (m, k // 32), dev), 0
+    ptrs = (xp, xs, _on(w, "w", u8, (n, k // 2), dev), _on(w_scales, "w_scales", u8, (n, k // 32), dev),
             _view(y, "y", torch.bfloat16, (m, n), dev))
     _call("kda_mx4_proj", lib.kda_mx4_proj, dev, stream, ptrs, (m, k, n, row, _row_stride(y, "y")))
 
@@ -864,14 +858,17 @@ def kda_mx4_moe(x, router, router_bias, w_up, w_up_scales, w_down, w_down_scales
     if scoring not in _SCORING:
         raise ValueError(f"scoring must be sigmoid or softmax, got {scoring!r}")
     size = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
+    u8 = torch.uint8
     ptrs = (_view(x, "x", bf, rows, dev), _on(router, "router", bf, (experts, k), dev),
             None if router_bias is None else _on(router_bias, "router_bias", torch.float32, (experts,), dev),
-            *_mx4(w_up, w_up_scales, ("w_up", "w_up_scales"), (every, twice, k), dev),
-            *_mx4(w_down, w_down_scales, ("w_down", "w_down_scales"), (every, k, inter), dev),
+            _on(w_up, "w_up", u8, (every, twice, k // 2), dev),
+            _on(w_up_scales, "w_up_scales", u8, (every, twice, k // 32), dev),
+            _on(w_down, "w_down", u8, (every, k, inter // 2), dev),
+            _on(w_down_scales, "w_down_scales", u8, (every, k, inter // 32), dev),
             None if state_indices is None else _on(state_indices, "state_indices", torch.int32, (m,), dev),
             _view(out, "out", bf, rows, dev), _on(expert_ids, "expert_ids", torch.int32, (m, top), dev),
             _on(expert_gates, "expert_gates", torch.float32, (m, top), dev),
-            _on(workspace, "workspace", torch.uint8, (size,), dev))
+            _on(workspace, "workspace", u8, (size,), dev))
     _call("kda_mx4_moe", lib.kda_mx4_moe, dev, stream, ptrs,
           (m, k, inter, experts, shared, top, _row_stride(x, "x"), _row_stride(out, "out"), _SCORING[scoring],
            1 if renormalise else 0, route_scale, size))

@@ -484,27 +484,27 @@ __global__ __launch_bounds__(64 * kWaves, 4) void up_kernel(MoeParams p) {
   }
 }
 
-template <int RQ, int U, bool TINY>
+template <int RQ, int STEPS, int U, bool TINY>
 __global__ __launch_bounds__(64 * kWaves, 4) void down_kernel(MoeParams p) {
   extern __shared__ __align__(16) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int n0 = blockIdx.x * 16, part = blockIdx.y;
-  const int nb = p.I / kMxBlock, units = (nb + 3) / 4;
+  const int nb = p.I / kMxBlock, units = (nb + 4 * STEPS - 1) / (4 * STEPS);
   const uint32_t jobs = scalar(p.head)[1] * units;
   // this wave's run of (slot, unit of k)
   const uint32_t share = part * kWaves + wave, shares = p.parts * kWaves;
   const int first = jobs * share / shares, end = jobs * (share + 1) / shares;
-  constexpr int kWave = RQ * 1024 + kPieceLds<1>;
-  char *hl = lds + wave * kWave, *wl = hl + RQ * 1024;
+  constexpr int kH = STEPS * RQ * 1024, kWave = kH + kPieceLds<STEPS>;
+  char *hl = lds + wave * kWave, *wl = hl + kH;
   // [wave][token][16]: this wave's sums
   f32x4* y = reinterpret_cast<f32x4*>(lds + kWaves * kWave) + wave * p.M * 4;
   for (int i = lane; i < p.M * 4; i += 64) y[i] = f32x4{};
   wave_lds_fence();
   if (first < end) {
     struct Unit {
-      Piece<1> w;
-      XRows<RQ> hi, lo;
+      Piece<STEPS> w;
+      XRows<RQ> hi[STEPS], lo[STEPS];
     } buf[U];
     // what is loaded next
     const uint32_t row_bytes = p.I / 2, code_row = (lane >> 2) * row_bytes, scale_row = (lane >> 2) * nb;
@@ -526,9 +526,12 @@ __global__ __launch_bounds__(64 * kWaves, 4) void down_kernel(MoeParams p) {
     };
     const auto load = [&](Unit& b) {
       if (job == end) return;
-      load_piece<1, TINY>(b.w, codes, code_row, scales, scale_row, nb, unit, lane & 3);
-      load_x<RQ>(b.hi, hi, row, unit * 128, p.I, l16, n_load);
-      load_x<RQ>(b.lo, lo, row, unit * 128, p.I, l16, n_load);
+      load_piece<STEPS, TINY>(b.w, codes, code_row, scales, scale_row, nb, unit, lane & 3);
+#pragma unroll
+      for (int j = 0; j < STEPS; ++j) {
+        load_x<RQ>(b.hi[j], hi, row, (unit * STEPS + j) * 128, p.I, l16, n_load);
+        load_x<RQ>(b.lo[j], lo, row, (unit * STEPS + j) * 128, p.I, l16, n_load);
+      }
       if (++job < end && ++unit == units) {
         unit = 0;
         ++slot;
@@ -537,21 +540,32 @@ __global__ __launch_bounds__(64 * kWaves, 4) void down_kernel(MoeParams p) {
     };
     f32x4 acc = {};
     const auto use = [&](Unit& b, int unit) {
-      stage_piece<1, TINY>(wl, b.w, nb, unit, lane);
-      stage_x<RQ>(hl, b.hi, unit * 128, p.I, l16, g, n_use);
-      wave_lds_fence();
-      const float sc = scale_of(scale_operand<1>(wl, 0, l16, g));
-      const u32x4 c = codes_operand(wl, 0, l16, g);
-      bf16x8 w[4];
+      stage_piece<STEPS, TINY>(wl, b.w, nb, unit, lane);
 #pragma unroll
-      for (int d = 0; d < 4; ++d) w[d] = dequant8(c[d], sc);
-#pragma unroll
-      for (int d = 0; d < 4; ++d) acc = mfma32(w[d], x_operand<RQ>(hl, d, l16, g), acc);
+      for (int j = 0; j < STEPS; ++j)
+        stage_x<RQ>(hl + j * (RQ * 1024), b.hi[j], (unit * STEPS + j) * 128, p.I, l16, g, n_use);
       wave_lds_fence();
-      stage_x<RQ>(hl, b.lo, unit * 128, p.I, l16, g, n_use);
+      bf16x8 w[STEPS][4];
+#pragma unroll
+      for (int j = 0; j < STEPS; ++j) {
+        const float sc = scale_of(scale_operand<STEPS>(wl, j, l16, g));
+        const u32x4 c = codes_operand(wl, j, l16, g);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) w[j][d] = dequant8(c[d], sc);
+      }
+      const auto multiply = [&]() {
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j)
+#pragma unroll
+          for (int d = 0; d < 4; ++d) acc = mfma32(w[j][d], x_operand<RQ>(hl + j * (RQ * 1024), d, l16, g), acc);
+      };
+      multiply();
       wave_lds_fence();
 #pragma unroll
-      for (int d = 0; d < 4; ++d) acc = mfma32(w[d], x_operand<RQ>(hl, d, l16, g), acc);
+      for (int j = 0; j < STEPS; ++j)
+        stage_x<RQ>(hl + j * (RQ * 1024), b.lo[j], (unit * STEPS + j) * 128, p.I, l16, g, n_use);
+      wave_lds_fence();
+      multiply();
       wave_lds_fence();
     };
     int at = first, at_slot = slot0, at_unit = unit;
@@ -661,12 +675,12 @@ MoeLayout moe_layout(int M, int K, int I, int E, int S, int top) {
 
 hipError_t launch_moe(const MoeParams& params, int cus, hipStream_t st) {
   MoeParams p = params;
-  // Tokens per slot.  4, with two units of k in flight, where an expert that is hit has
-  // about one: us with 4 / 16, 7168 x 512 x 256 experts, 8 + 1 of them a token: 16 tokens
-  // 126 / 152, 64 tokens 288 / 279; 2048 x 1024 x 128 experts, 8 a token: 16 tokens 68 / 72,
-  // 32 tokens 94 / 91; 8 experts, 64 tokens 46 / 36.  What has more tokens than a slot is read
-  // once for each slot, from the L2 mostly: by workgroups that run at the same time.
-  p.chunk = p.M <= 4 || p.M * p.top <= p.E ? 4 : 16;
+  // Tokens per slot: 4 where an expert that is hit has about two at most.  us with 4 / 16,
+  // all experts as likely: 7168 x 512, 8 + 1 of 256 experts, 16 tokens 155 / 200, 64 tokens
+  // 341 / 406; 2048 x 1024, 8 of 128, 32 tokens 104 / 114, 64 tokens 149 / 135; 2080 x 1056,
+  // 4 of 40, 32 tokens 75 / 70.  What has more tokens than a slot is read once for each
+  // slot, from the L2 mostly: by workgroups that run at the same time.
+  p.chunk = p.M <= 4 || p.M * p.top <= 2 * p.E ? 4 : 16;
   p.parts = moe_parts(p.M, p.K, p.I, p.E, p.S, p.top, p.chunk);
   void* args[] = {&p};
   const auto go = [&](auto* f, dim3 grid, int threads, size_t lds) {
@@ -682,18 +696,20 @@ hipError_t launch_moe(const MoeParams& params, int cus, hipStream_t st) {
   while ((int64_t(1) << p.up_log2) < items && (2 << p.up_log2) <= 2 * cus) ++p.up_log2;
   const dim3 up(1u << p.up_log2), down(p.K / 16, p.parts);
   const size_t sums = size_t(kWaves) * p.M * 64;
-  // With 16 tokens a slot one unit of k in flight leaves registers for another workgroup:
-  // 64 x 2080 x 1056, 40 experts 79 us against 85 with two, 64 x 7168 x 512, 256 experts
-  // 273 against 286.
+  // Units of 256 of k with 4 tokens a slot: a unit costs about 100 instructions whatever
+  // its size, and down of 64 tokens, 7168 x 512, 256 experts, took 139 us with 128.  One in
+  // flight, but two in up, whose items are shorter: registers for other waves fill the time
+  // as well as loads ahead do (16 tokens a slot, 64 x 2080 x 1056, 40 experts 79 us against
+  // 85 with two).
   if (p.chunk == 4) {
     e = go(p.K < 128 ? &up_kernel<1, 2, 2, true> : &up_kernel<1, 2, 2, false>, up, 64 * kWaves, 0);
     if (e != hipSuccess) return e;
-    return go(p.I < 128 ? &down_kernel<1, 4, true> : &down_kernel<1, 4, false>, down, 64 * kWaves,
-              sums + kWaves * (1024 + kPieceLds<1>));
+    return go(p.I < 128 ? &down_kernel<1, 2, 1, true> : &down_kernel<1, 2, 1, false>, down, 64 * kWaves,
+              sums + kWaves * (2048 + kPieceLds<2>));
   }
   e = go(p.K < 128 ? &up_kernel<4, 1, 1, true> : &up_kernel<4, 1, 1, false>, up, 64 * kWaves, 0);
   if (e != hipSuccess) return e;
-  return go(p.I < 128 ? &down_kernel<4, 1, true> : &down_kernel<4, 1, false>, down, 64 * kWaves,
+  return go(p.I < 128 ? &down_kernel<4, 1, 1, true> : &down_kernel<4, 1, 1, false>, down, 64 * kWaves,
             sums + kWaves * (4096 + kPieceLds<1>));
 }
 

@@ -126,7 +126,7 @@ __device__ __forceinline__ void load_x(XRows<RQ>& x, const uint16_t* base, const
   const int rest = (K - 8 - k0) >> 3;
 #pragma unroll
   for (int q = 0; q < RQ; ++q)
-    if (4 * q < n)
+    if (RQ == 1 || 4 * q < n)
       x.v[q] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(at) + (row[q] + uint32_t(min(l16, rest)) * 16));
 }
 // Pieces behind the end of k (they repeat another) as zeros.
@@ -141,7 +141,7 @@ __device__ __forceinline__ void stage_x(char* lds, XRows<RQ>& x, int k0, int K, 
 #pragma unroll
   for (int q = 0; q < RQ; ++q) {
     const int r = 4 * q + g;
-    if (4 * q < n) *reinterpret_cast<u32x4*>(lds + r * 256 + ((l16 ^ r) << 4)) = x.v[q];
+    if (RQ == 1 || 4 * q < n) *reinterpret_cast<u32x4*>(lds + r * 256 + ((l16 ^ r) << 4)) = x.v[q];
   }
 }
 // (rows that are not staged repeat those that are: their columns are not used)
