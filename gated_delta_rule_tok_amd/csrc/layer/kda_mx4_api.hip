@@ -81,6 +81,8 @@ kda_status_t kda_mx4_proj(const void* x, const void* x_scales, const void* w, co
   if (num_tokens > 0 && (!x || !y)) return KDA_ERR_INVALID_ARG;
   if (!x_scales && (num_tokens > 64 || !rows_ok(num_tokens, x_row, k, 1 << 24))) return KDA_ERR_INVALID_ARG;
   if (num_tokens > 1 && (y_row < n || y_row > (int64_t(1) << 30))) return KDA_ERR_INVALID_ARG;
+  // a grid holds fewer than 2^32 threads: 512 for a tile
+  if (((num_tokens + 255) / 256) * ((n + 255) / 256) >= (int64_t(1) << 23)) return KDA_ERR_INVALID_ARG;
   if (num_tokens == 0) return KDA_OK;
   kda::Mx4Params p{};
   p.x = x;

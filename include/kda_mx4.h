@@ -39,17 +39,17 @@ extern "C" {
  *   x       bf16 [num_rows, k], rows x_row elements apart
  *   codes, scales  as above; codes 4-byte aligned
  *
- * k is a positive multiple of 32, at most 2^20; 0 <= num_rows < 2^31; x 16-byte
- * aligned, x_row a multiple of 8 between k and 2^30 (for one row any).
+ * k is a positive multiple of 32, at most 2^20; 0 <= num_rows < 2^31, num_rows * k
+ * below 2^36; x 16-byte aligned, x_row a multiple of 8 between k and 2^30 (for one
+ * row any).  Nothing overlaps.
  */
 kda_status_t kda_mx4_quant(const void* x, void* codes, void* scales, void* stream, int64_t num_rows,
                            int32_t k, int64_t x_row);
 
 /*
  * The values of codes and scales as bf16 [num_rows, k], rows out_row elements
- * apart.  Exact, except that 4 and 6 times 2^127 (s = 254, and 6 times 2^126 is
- * still exact) are infinite.  Limits as for the quantisation; out 16-byte, codes
- * 4-byte aligned.
+ * apart.  Exact, except that values of 2^128 and more (s = 253 and 254) are
+ * infinite.  Limits as for the quantisation; out 16-byte, codes 4-byte aligned.
  */
 kda_status_t kda_mx4_dequant(const void* codes, const void* scales, void* out, void* stream,
                              int64_t num_rows, int32_t k, int64_t out_row);
@@ -65,11 +65,12 @@ kda_status_t kda_mx4_dequant(const void* codes, const void* scales, void* out, v
  *
  * k is a positive multiple of 32, at most 2^20; 1 <= n <= 2^24; x and w are
  * 16-byte aligned; x_row a multiple of 8 between k and 2^24, y_row between n and
- * 2^30 (for one row any).  y must not overlap x or w.
+ * 2^30 (for one row any); ceil(num_tokens / 256) * ceil(n / 256) < 2^23.  y must
+ * not overlap x or w.
  *
- * Every product is exact, sums are fp32 (a sum of 128 products at a time in one
- * instruction, whose own sum is off by less than 2^-24 of the products'
- * magnitudes).  A value of x that is not finite, or a scale of NaN, makes its
+ * Every product is exact (with bf16 x of weights below 2^128, which bf16 holds),
+ * sums are fp32 (up to 128 products at a time in one instruction, whose own sum
+ * is off by less than 2^-24 of the products' magnitudes).  A value of x that is not finite, or a scale of NaN, makes its
  * token's row of y, or its weight row's column, NaN or infinite; others are not
  * affected.  The order of a sum may depend on num_tokens, and on nothing else of
  * the other tokens.  No workspace.  x and y may be NULL when num_tokens is 0.

@@ -340,6 +340,22 @@ def test_proj_of_any_size(m, k, n, size):
         _check_product(b.double(), w, ws, y, f"bf16 2^{size}")
 
 
+@pytest.mark.parametrize("m", [1, 16, 40])
+def test_proj_of_the_least_weights(m):
+    """Scales of 2^-127 and a little above, whose values bf16 holds as subnormals."""
+    import torch
+    k, n = 256, 48
+    w, _ = _weights((n,), k, 16)
+    ws = torch.randint(0, 4, (n, k // 32), generator=_gen(17), device="cuda", dtype=torch.uint8)
+    x = torch.randn(m, k, generator=_gen(18), device="cuda").mul(2.0 ** 100).bfloat16()
+    y = torch.full((m, n), math.nan, dtype=torch.bfloat16, device="cuda")
+    _kda().kda_mx4_proj(x, None, w, ws, y)
+    _check_product(x.double(), w, ws, y, "least weights")
+    c, s = _run_quant(x)
+    _kda().kda_mx4_proj(c, s, w, ws, y)
+    _check_product(_values(c, s), w, ws, y, "least weights, codes")
+
+
 def test_proj_of_no_rows():
     import torch
     w, ws = _weights((5,), 64, 15)
@@ -536,14 +552,14 @@ def test_moe_of_what_is_not_finite():
 def test_moe_rows_do_not_depend_on_the_tokens_beside():
     import torch
     p = Moe(30, 1024, 128, 12, 3, 1, False, seed=35)
-    p.run()
-    y = p.out[11].clone()
+    p.run().check("first tokens")
+    ids, gates = p.ids[11].clone(), p.gates[11].clone()
     x = p.x[11].clone()
     p.x[:] = torch.randn(30, 1024, generator=_gen(36), device="cuda").bfloat16()
     p.x[11] = x
     p.run().check("other tokens")
-    # (its experts' lists are longer or shorter, so that its sums over experts are in another order)
-    assert ((p.out[11].double() - y.double()).abs() <= 2.0 ** -7 * y.double().abs() + 1e-4).all()
+    # the choice and its gates to the bit (sums over experts may be in another order)
+    assert torch.equal(p.ids[11], ids) and torch.equal(p.gates[11], gates)
 
 
 def test_moe_of_no_tokens():

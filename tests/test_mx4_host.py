@@ -57,7 +57,7 @@ def _proj(**over):
     {"x": None}, {"w": None}, {"ws": None}, {"y": None}, {"x": FAKE + 8}, {"w": FAKE + 8}, {"y": FAKE + 1},
     {"m": -1}, {"m": 65}, {"m": 1 << 31, "xs": FAKE}, {"k": 0}, {"k": 40}, {"k": 1 << 21}, {"n": 0},
     {"n": (1 << 24) + 1}, {"x_row": 248}, {"x_row": 260}, {"x_row": 1 << 25}, {"y_row": 39}, {"y_row": 1 << 31},
-    {"xs": FAKE, "x": FAKE + 4},
+    {"xs": FAKE, "x": FAKE + 4}, {"xs": FAKE, "m": (1 << 31) - 1, "n": 257, "y_row": 257},
 ], ids=str)
 def test_proj_refusals(over):
     assert _proj(**over) == INVALID
