@@ -98,9 +98,7 @@ kda_status_t kda_mx4_proj(const void* x, const void* x_scales, const void* w, co
   int cus = 0;
   if (hipError_t e = kda::device_cus(&cus); e != hipSuccess) return failed(e, "device query");
   hipStream_t st = static_cast<hipStream_t>(stream);
-  // Tiles through LDS against the streaming form (us): 512 x 2048 x 2048 8.0 / 9.6, 128 x
-  // 7168 x 7168 22 / 21, 300 x 4128 x 2050 17.9 / 16.1, 512 x 7168 x 1536 18.7 / 15.0.
-  const bool tile = p.xs && num_tokens > 64 && num_tokens * n >= 1 << 20;
+  const bool tile = p.xs && kda::mx4_in_tiles(p, cus);
   if (hipError_t e = tile ? kda::launch_mx4_tile(p, cus, st) : kda::launch_mx4_few(p, cus, st); e != hipSuccess)
     return failed(e, "4-bit product launch");
   return KDA_OK;

@@ -247,7 +247,7 @@ hipError_t few_mx4(const Mx4Params& p, hipStream_t st) {
 //    2048 x 7168 9.1 / 8.4, 64 x 2048 x 2048 8.8 / 4.6.  32: 30 x 7168 x 14336 29.4 / 33.4,
 //    but 32 x 7168 x 1536 11.9 / 8.1.  With x in the format 32 and one unit in flight for
 //    all of more than 16 tokens: 64 x 7168 x 1536 7.4 against 8.2 with 32 rows in two
-//    units, 17.7 with 64 x 64; 300 x 4128 x 2050 16.1 / 19.4 / 18.0.
+//    units, 17.7 with 64 x 64 (larger calls go to kda_mx4_tile.hip).
 hipError_t launch_mx4_few(const Mx4Params& p, int cus, hipStream_t stream) {
   const int64_t rows16 = (p.N + 15) / 16, rows32 = (p.N + 31) / 32, rows64 = (p.N + 63) / 64;
   if (p.xs) {

@@ -26,6 +26,8 @@ struct Mx4Params {
   int K, N;
 };
 hipError_t launch_mx4_few(const Mx4Params& p, int cus, hipStream_t stream);
+// Whether rows of x in the format are worth tiles through LDS.
+bool mx4_in_tiles(const Mx4Params& p, int cus);
 hipError_t launch_mx4_tile(const Mx4Params& p, int cus, hipStream_t stream);
 
 // One call of the mixture-of-experts layer.  A pair is a token and an expert that

@@ -1,12 +1,11 @@
 // kda_mx4_tile.hip -- products of many rows x with weights, both in microscaled
 // 4-bit numbers:  y[m, n] = sum_k x[m, k] w[n, k].
 //
-// Bound by the scaled 4-bit MFMA (32x32x64: 32 cycles).  A workgroup of four waves
-// makes BM x BN outputs, each wave a quarter, from operands in LDS: stages of 128 of k
-// that loads fill directly, three or seven ahead of the one in use, and the scales of
-// 512 of k at a time.  A wave of 128 x 128 outputs reads 8 KB of LDS for 16 MFMAs, 64 of
-// LDS's 128 bytes a cycle with four waves; it has the operands of its next 16 MFMAs on
-// the way while it issues 16, over the barrier between stages too.
+// Bound by the scaled 4-bit MFMA (32x32x64: 32 cycles) where there are many rows.  A
+// workgroup makes BM x BN outputs from operands in LDS: stages of 128 of k that loads
+// fill directly, three or seven ahead of the one in use, and the scales of 512 of k at a
+// time.  A wave has the operands of its next half stage on the way while it issues the
+// MFMAs of one, over the barrier between stages too.
 //
 // The loads are written in assembly: with the builtin the compiler waits for every
 // load into LDS before each read of it, which leaves one stage in flight.  Their
@@ -309,9 +308,26 @@ hipError_t launch(const Mx4Params& p, hipStream_t st) {
 
 }  // namespace
 
+static int64_t tiles_of(const Mx4Params& p, int side) {
+  return ((p.M + side - 1) / side) * ((p.N + side - 1) / side);
+}
+
+// Tiles of 64 x 64 and more against the streaming form (us, 64 x 64 / streaming): where
+// they are half the compute units and more, 128 x 2048 x 4096 5.8 / 6.0, 64 x 7168 x 8200
+// 18.8 / 20.4, 64 x 7168 x 14336 20 / 29, 300 x 4128 x 2050 11.6 / 16.3, 512 x 7168 x 1536
+// 13.2 / 15.2, but 128 x 7168 x 1536 (48 tiles) 13.1 / 6.9, 64 x 7168 x 7168 (112) 18.6 /
+// 16.7; with 32 tokens and fewer half a tile's work is for nothing: 32 x 7168 x 8200 15.4 /
+// 14.8, 20 x 2080 x 12000 9.3 / 8.2.
+bool mx4_in_tiles(const Mx4Params& p, int cus) { return p.M > 32 && 2 * tiles_of(p, 64) >= cus; }
+
+// The side of a tile (us, 64 / 128 / 256): the smallest that two workgroups a compute unit
+// (of 64), one (of 128) hold at once: a stage's round trip counts, not its MFMAs.  512 x
+// 2048 x 2048 5.9 / 8.0 / 14.7, 256 x 7168 x 7168 18.6 / 21.6 / 42, 1024 x 7168 x 1536 15.7 /
+// 22.4; 300 x 2080 x 8200 18.4 / 11.6 / 17.7, 512 x 7168 x 7168 35 / 24.8 / 43; 1024 x 7168 x
+// 7168 - / 46 / 44, 2048 x 2048 x 7168 - / 33 / 22.
 hipError_t launch_mx4_tile(const Mx4Params& p, int cus, hipStream_t stream) {
-  const int64_t small = ((p.M + 127) / 128) * ((p.N + 127) / 128);
-  if (small <= cus) return launch<128, 128, 8, 2>(p, stream);
+  if (tiles_of(p, 64) <= 2 * cus) return launch<64, 64, 8, 1>(p, stream);
+  if (tiles_of(p, 128) <= cus) return launch<128, 128, 8, 2>(p, stream);
   return launch<256, 256, 4, 4>(p, stream);
 }
 

@@ -203,7 +203,8 @@ def test_proj_of_codes(m, k, n):
 # rows and columns of tiles in part, more tiles than compute units
 TILES = [(1024, 32, 1030), (1100, 96, 1000), (1024, 128, 1024), (1025, 160, 1030), (2000, 256, 600), (1030, 416, 1024),
          (1024, 480, 1030), (1024, 512, 1024), (1030, 640, 1100), (129, 896, 8200), (8200, 1152, 130),
-         (1024, 2080, 1100), (4500, 544, 4400), (4300, 1024, 4400), (70, 2048, 15000), (5000, 64, 5000)]
+         (1024, 2080, 1100), (4500, 544, 4400), (4300, 1024, 4400), (70, 2048, 15000), (5000, 64, 5000),
+         (33, 160, 8192), (50, 2048, 8300), (64, 544, 9000), (700, 4128, 800), (300, 512, 2050), (2000, 1056, 1000)]
 
 
 @pytest.mark.parametrize("shift", [0, 1])
