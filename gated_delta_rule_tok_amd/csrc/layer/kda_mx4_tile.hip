@@ -59,9 +59,10 @@ __device__ __forceinline__ void wait_loads() {  // at most N loads under way, an
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(N) : "memory");
 }
 
-// WN: waves along w's rows; two along x's.  DIRECT: scales by loads into LDS too, where
-// each row's are at 4-byte addresses, at least 16, and the stages whole; otherwise
-// through registers, whose wait empties the wave's loads once in four stages.
+// WN: waves along w's rows; two along x's.  DIRECT: each row's scales are at 4-byte
+// addresses, and the stages whole.  Otherwise the words around them are loaded, and a
+// stage's scales put together from two: 4096 x 4128 x 4096 47 us (50 by
+// way of registers, whose wait empties the wave's loads once in four stages).
 template <int BM, int BN, int NS, int WN, bool DIRECT>
 __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
   constexpr int kWaves = 2 * WN;
@@ -88,9 +89,14 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
   const uint32_t row_bytes = p.K / 2, nb = p.K / kMxBlock;
   const uint64_t m_left = uint64_t(p.M - m0), n_left = uint64_t(p.N - n0);
   const uint8_t *xs = p.xs + size_t(m0) * nb, *ws = p.ws + size_t(n0) * nb;
+  // bytes of the first row's scales behind a word's begin (what is read of the words beside
+  // an operand's scales is not used)
+  const uint32_t x_turn = DIRECT ? 0 : reinterpret_cast<uintptr_t>(xs) & 3,
+                 w_turn = DIRECT ? 0 : reinterpret_cast<uintptr_t>(ws) & 3;
   const i32x4 xb = rsrc_of(static_cast<const uint8_t*>(p.x) + size_t(m0) * row_bytes, m_left * row_bytes),
               wb = rsrc_of(p.w + size_t(n0) * row_bytes, n_left * row_bytes),
-              xsb = rsrc_of(xs, m_left * nb), wsb = rsrc_of(ws, n_left * nb);
+              xsb = rsrc_of(xs - x_turn, (x_turn + m_left * nb + 3) & ~uint64_t(3)),
+              wsb = rsrc_of(ws - w_turn, (w_turn + n_left * nb + 3) & ~uint64_t(3));
   const int mlast = int(p.M - 1 - m0 < BM ? p.M - 1 - m0 : BM - 1), nlast = min(p.N - 1 - n0, BN - 1);
   // this lane's source of each load of a stage; rows behind the last repeat it
   uint32_t off[kLoads], soff[kScaleLoads];
@@ -103,7 +109,7 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
 #pragma unroll
   for (int i = 0; i < kScaleLoads; ++i) {
     const int r = (wave * kScaleLoads + i) * 64 + lane;
-    soff[i] = uint32_t(r < BM ? min(r, mlast) : min(r - BM, nlast)) * nb;
+    soff[i] = (r < BM ? x_turn + min(r, mlast) * nb : w_turn + min(r - BM, nlast) * nb) & ~3u;
   }
   const int T = (nb + 3) / 4;
   // (a wave's loads are all of x or all of w)
@@ -116,34 +122,12 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
   const auto issue = [&](int t, int i) {
     load_lds(code_base, off[i], min(t, T - 1) * 64, code0 + (t & (NS - 1)) * sizeof(L.code[0]), i * 1024);
   };
-  // The scales of four stages are 16 bytes a row; the last ones of a row are its last
-  // 16 bytes, so that no load passes its end.
-  u32x4 held;  // 16 scales of this thread's row, on their way
-  static_assert(BM + BN == 64 * kWaves, "a row each");
-  const auto load_scales = [&](int t) {
-    const int r = threadIdx.x;
-    const uint8_t* at = (r < BM ? xs + size_t(min(r, mlast)) * nb : ws + size_t(min(r - BM, nlast)) * nb) + 4 * t;
-    held = u32x4{};
-    if (4 * t + 16 <= int(nb)) {
-      struct __attribute__((packed, aligned(1))) B { uint32_t v[4]; };
-      const B b = *reinterpret_cast<const B*>(at);
-      held = u32x4{b.v[0], b.v[1], b.v[2], b.v[3]};
-    } else {  // the row's last ones: zeros behind them, so that what is read of its codes there counts nothing
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (4 * t + i < int(nb)) held[i / 4] |= uint32_t(at[i]) << (8 * (i & 3));
-    }
-  };
-  const auto store_scales = [&](int t) {
-    *reinterpret_cast<u32x4*>(L.scale[(t >> 2) & (L.kScales - 1)] + threadIdx.x * 16) = held;
-  };
+  // The scales of four stages are 16 bytes a row (or the words where they begin).
   const auto issue_scales = [&](int t) {
-    if ((t & 3) || t >= T) return;
+    if ((t & 3) || t > T) return;  // (the word behind a row's last may be wanted)
 #pragma unroll
-    for (int i = 0; i < kScaleLoads; ++i) {
-      load_lds(scale_base, soff[i], min(uint32_t(4 * t), nb - 16),
-               scale0 + ((t >> 2) & (L.kScales - 1)) * sizeof(L.scale[0]), i * 1024);
-    }
+    for (int i = 0; i < kScaleLoads; ++i)
+      load_lds(scale_base, soff[i], 4 * t, scale0 + ((t >> 2) & (L.kScales - 1)) * sizeof(L.scale[0]), i * 1024);
   };
   f32x16 acc[FM][FN] = {};
   const int xr = wave / WN * (BM / 2) + l32, wr = BM + wave % WN * (BN / WN) + l32;  // rows of the stage
@@ -152,7 +136,7 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
   } f[2];
   struct Scales {
     uint32_t x[FM], w[FN];
-  } sc;
+  } sc, word;
   // fragment i of stage t, half s (0, 1): w's, then x's
   const auto read = [&](Frags& f, int t, int s, int i) {
     const int r = i < FN ? wr + 32 * i : xr + 32 * (i - FN);
@@ -163,16 +147,33 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
       f.b[i - FN] = v;
   };
   const auto read_scale = [&](Scales& o, int t, int i) {
-    t = min(t, T - 1);
-    // this stage's in the row's 16 bytes
-    const int at = DIRECT ? 4 * t - int(min(uint32_t(4 * (t & ~3)), nb - 16)) : 4 * (t & 3);
     const int r = i < FN ? wr + 32 * i : xr + 32 * (i - FN);
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(L.scale[(t >> 2) & (L.kScales - 1)] + at + r * 16);
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(L.scale[(t >> 2) & (L.kScales - 1)] + 4 * (t & 3) + r * 16);
     if (i < FN)
       o.w[i] = v;
     else
       o.x[i - FN] = v;
   };
+  // A stage's scales, shifted for this lane's half, from the word that was read last; where
+  // the rows are not at word addresses from that and the one before it, with zeros behind
+  // the row's end, so that what is read of its codes there counts nothing.
+  const uint32_t turn_w = (w_turn + (wr - BM) * nb) & 3, turn_x = (x_turn + xr * nb) & 3;  // (32 rows on the same)
+  const uint32_t end_mask = nb & 3 ? (1u << (8 * (nb & 3))) - 1 : ~0u;
+  const auto scales_of = [&](const Scales& read, int t) {
+    const uint32_t mask = t == T - 1 ? end_mask : ~0u;
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      sc.w[i] = DIRECT ? read.w[i] : __builtin_amdgcn_alignbyte(read.w[i], word.w[i], turn_w) & mask;
+      sc.w[i] >>= 8 * half;
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      sc.x[i] = DIRECT ? read.x[i] : __builtin_amdgcn_alignbyte(read.x[i], word.x[i], turn_x) & mask;
+      sc.x[i] >>= 8 * half;
+    }
+    word = read;
+  };
+  constexpr int kAhead = DIRECT ? 0 : 1;  // the word that completes stage t's scales: t + kAhead
   // The products of one half stage; between(n) is issued behind the n-th of them: a wave
   // alone on its SIMD issues everything else in the MFMAs' time or instead of them.
   const auto multiply = [&](const Frags& f, auto s, const Scales& c, const auto& between) {
@@ -190,14 +191,10 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
   };
 #pragma unroll
   for (int t = 0; t < NS; ++t) {
-    if (DIRECT) issue_scales(t);
+    issue_scales(t);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       if (t + 1 < NS || i < kLoads - kLoads / 2) issue(t, i);  // (the rest comes in the loop)
-  }
-  if (!DIRECT) {
-    load_scales(0);
-    store_scales(0);
   }
   wait_loads<(NS - 2) * kLoads>();  // the first stage
   __builtin_amdgcn_s_barrier();
@@ -206,28 +203,19 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
 #pragma unroll
   for (int i = 0; i < kReads; ++i) {
     read(f[0], 0, 0, i);
-    read_scale(sc, 0, i);
+    if (!DIRECT) read_scale(word, 0, i);
   }
-  const auto shift = [&](Scales& c) {
+  Scales next;
 #pragma unroll
-    for (int i = 0; i < FN; ++i) c.w[i] >>= 8 * half;
-#pragma unroll
-    for (int i = 0; i < FM; ++i) c.x[i] >>= 8 * half;
-  };
-  shift(sc);
+  for (int i = 0; i < kReads; ++i) read_scale(next, kAhead, i);
+  scales_of(next, 0);
   // Reads in the first half of a half stage's MFMAs, loads in the second half: those of
   // stage t + NS where stage t's last read is done, the rest in front of the next wait.
   constexpr int kEach = (2 * kReads + kSlots - 1) / kSlots, kLoadsEach = (kLoads + kSlots - 1) / kSlots;
   constexpr int kLate = kLoads / 2;  // of a stage's loads, in the next one's time
   for (int t = 0; t < T; ++t) {
     // (the one branch, in front: the compiler moves MFMAs behind one, all at once)
-    if (DIRECT) {
-      if (t) issue_scales(t + NS - 1);
-    } else if ((t & 3) == 0) {
-      if (t + 4 < T) load_scales(t + 4);
-    } else if ((t & 3) == 3) {
-      if (t + 1 < T) store_scales(t + 1);
-    }
+    issue_scales(t + NS);
     multiply(f[0], std::integral_constant<int, 0>{}, sc, [&](int n) {
 #pragma unroll
       for (int i = n * kEach; i < (n + 1) * kEach && i < kReads; ++i) read(f[1], t, 1, i);
@@ -240,19 +228,17 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
     wait_loads<(NS - 2) * kLoads>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    Scales next;
     multiply(f[1], std::integral_constant<int, 1>{}, sc, [&](int n) {
 #pragma unroll
       for (int i = n * kEach; i < (n + 1) * kEach && i < kReads; ++i) {
         read(f[0], t + 1, 0, i);
-        read_scale(next, t + 1, i);
+        read_scale(next, t + 1 + kAhead, i);
       }
 #pragma unroll
       for (int i = (n - kSlots / 2) * kLoadsEach; i < (n - kSlots / 2 + 1) * kLoadsEach; ++i)
         if (i >= 0 && i < kLoads - kLate) issue(t + NS, i);
     });
-    shift(next);
-    sc = next;
+    scales_of(next, t + 1);
   }
   wait_loads<0>();
   // y by rows of 16-byte pieces, through LDS: 32 tokens of this wave at a time
@@ -297,7 +283,7 @@ __global__ __launch_bounds__(128 * WN) void tile_kernel(Mx4Params p) {
 template <int BM, int BN, int NS, int WN>
 hipError_t launch(const Mx4Params& p, hipStream_t st) {
   const auto at = [](const void* q) { return reinterpret_cast<uintptr_t>(q); };
-  const bool direct = p.K % 128 == 0 && p.K >= 512 && at(p.xs) % 4 == 0 && at(p.ws) % 4 == 0;
+  const bool direct = p.K % 128 == 0 && at(p.xs) % 4 == 0 && at(p.ws) % 4 == 0;
   const void* f = direct ? reinterpret_cast<const void*>(&tile_kernel<BM, BN, NS, WN, true>)
                          : reinterpret_cast<const void*>(&tile_kernel<BM, BN, NS, WN, false>);
   Mx4Params arg = p;
@@ -314,7 +300,7 @@ static int64_t tiles_of(const Mx4Params& p, int side) {
 
 // Tiles of 64 x 64 and more against the streaming form (us, 64 x 64 / streaming): where
 // they are half the compute units and more, 128 x 2048 x 4096 5.8 / 6.0, 64 x 7168 x 8200
-// 18.8 / 20.4, 64 x 7168 x 14336 20 / 29, 300 x 4128 x 2050 11.6 / 16.3, 512 x 7168 x 1536
+// 18.8 / 20.4, 64 x 7168 x 14336 20 / 29, 300 x 4128 x 2050 11.3 / 16.3, 512 x 7168 x 1536
 // 13.2 / 15.2, but 128 x 7168 x 1536 (48 tiles) 13.1 / 6.9, 64 x 7168 x 7168 (112) 18.6 /
 // 16.7; with 32 tokens and fewer half a tile's work is for nothing: 32 x 7168 x 8200 15.4 /
 // 14.8, 20 x 2080 x 12000 9.3 / 8.2.
@@ -323,7 +309,7 @@ bool mx4_in_tiles(const Mx4Params& p, int cus) { return p.M > 32 && 2 * tiles_of
 // The side of a tile (us, 64 / 128 / 256): the smallest that two workgroups a compute unit
 // (of 64), one (of 128) hold at once: a stage's round trip counts, not its MFMAs.  512 x
 // 2048 x 2048 5.9 / 8.0 / 14.7, 256 x 7168 x 7168 18.6 / 21.6 / 42, 1024 x 7168 x 1536 15.7 /
-// 22.4; 300 x 2080 x 8200 18.4 / 11.6 / 17.7, 512 x 7168 x 7168 35 / 24.8 / 43; 1024 x 7168 x
+// 22.4; 300 x 2080 x 8200 18.4 / 10.1 / 17.7, 512 x 7168 x 7168 35 / 24.8 / 43; 1024 x 7168 x
 // 7168 - / 46 / 44, 2048 x 2048 x 7168 - / 33 / 22.
 hipError_t launch_mx4_tile(const Mx4Params& p, int cus, hipStream_t stream) {
   if (tiles_of(p, 64) <= 2 * cus) return launch<64, 64, 8, 1>(p, stream);

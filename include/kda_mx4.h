@@ -70,10 +70,11 @@ kda_status_t kda_mx4_dequant(const void* codes, const void* scales, void* out, v
  *
  * Every product is exact (with bf16 x of weights below 2^128, which bf16 holds),
  * sums are fp32 (up to 128 products at a time in one instruction, whose own sum
- * is off by less than 2^-24 of the products' magnitudes).  A value of x that is not finite, or a scale of NaN, makes its
- * token's row of y, or its weight row's column, NaN or infinite; others are not
- * affected.  The order of a sum may depend on num_tokens, and on nothing else of
- * the other tokens.  No workspace.  x and y may be NULL when num_tokens is 0.
+ * is off by less than 2^-24 of the products' magnitudes).  A value of x that is not
+ * finite, or a scale of NaN, makes its token's row of y, or its weight row's column,
+ * NaN or infinite; others are not affected.  The order of a sum may depend on
+ * num_tokens, and on nothing else of the other tokens.  No workspace.  x and y may be
+ * NULL when num_tokens is 0.
  */
 kda_status_t kda_mx4_proj(const void* x, const void* x_scales, const void* w, const void* w_scales,
                           void* y, void* stream, int64_t num_tokens, int32_t k, int32_t n,

@@ -229,6 +229,24 @@ def test_proj_in_tiles(m, k, n, shift):
     assert torch.equal(y[:m, :n], y2)
 
 
+@pytest.mark.parametrize("xshift,wshift", [(0, 1), (2, 3), (3, 0)])
+@pytest.mark.parametrize("m,k,n", [(200, 928, 4100), (130, 960, 5000), (1000, 992, 1100), (2100, 992, 2060),
+                                   (300, 1024, 2050), (90, 1056, 8200)])
+def test_proj_in_tiles_between_nans(m, k, n, xshift, wshift):
+    """Scales at any byte, with NaN scales right before and behind them."""
+    import torch
+    x, xs = _weights((m,), k, m + k, spread=3)
+    w, ws = _weights((n,), k, n)
+
+    def moved(t, shift):
+        flat = torch.full((t.numel() + 32,), 0xFF, dtype=torch.uint8, device="cuda")
+        flat[shift:shift + t.numel()] = t.flatten()
+        return flat[shift:shift + t.numel()].view(t.shape)
+    y = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    _kda().kda_mx4_proj(x, moved(xs, xshift), w, moved(ws, wshift), y)
+    _check_product(_values(x, xs), w, ws, y, f"tiles {m}x{k}x{n}, scales at {xshift}, {wshift}")
+
+
 def test_proj_in_tiles_rows_do_not_mix():
     """NaN scales of one token and of one weight row stay in their row and column, also in
     the last blocks of k."""
