@@ -5,7 +5,7 @@
 //   logits   x router^T in fp64, (tile of 16 experts) x (slice of k) per workgroup
 //   route    a token per workgroup: slices joined, scores, choice; the last one to
 //            finish lists the experts that are hit and their tokens, as slots
-//   up       h = gate silu(G x) (U x), as two bf16 pieces: a workgroup walks through
+//   up       h = gate silu(G x) (U x), as three bf16 pieces: a workgroup walks through
 //            a run of (slot, 16 rows of G and of U), its waves share k
 //   down     16 rows of W_down of all slots per workgroup, or of a part of them where
 //            the rows are few; the sum over experts ends there
@@ -453,10 +453,17 @@ __global__ __launch_bounds__(64 * kWaves, 4) void up_kernel(MoeParams p) {
         for (int w = 1; w < kWaves; ++w) a += at[w * 512], u += at[w * 512 + 256];
         if (m < s.n) {
           const float h = a / (1.f + __expf(-a)) * u * gate;
-          const uint16_t top = f32_to_bf16(h);
-          const size_t o = size_t(s.begin + m) * p.I + at_tile * 16 + n;
-          p.h_hi[o] = top;
-          p.h_lo[o] = f32_to_bf16(h - bf16_to_f32(top));
+          // all 24 bits of h, 8 to a piece: cut, not rounded, so that the rest is exact and
+          // the first never passes bf16's largest
+          const size_t plane = size_t(p.M) * (p.top + p.S) * p.I;
+          uint16_t* o = p.h + size_t(s.begin + m) * p.I + at_tile * 16 + n;
+          float rest = h;
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const uint32_t piece = __float_as_uint(rest) & 0xffff0000u;
+            o[i * plane] = uint16_t(piece >> 16);
+            rest -= __uint_as_float(piece);
+          }
         }
       }
     }
@@ -492,6 +499,12 @@ __global__ __launch_bounds__(64 * kWaves, 4) void up_kernel(MoeParams p) {
   }
 }
 
+// The operands of h in LDS: with 4 tokens a slot the three pieces of a step as rows 4 i +
+// token, which are columns of one MFMA (and added up when the slot is done); with 16 one
+// piece of all steps after the other.
+template <int RQ, int STEPS>
+constexpr int kDownH = RQ == 1 ? 3 * 1024 : STEPS * RQ * 1024;
+
 template <int RQ, int STEPS, int U, bool TINY>
 __global__ __launch_bounds__(64 * kWaves, 4) void down_kernel(MoeParams p) {
   extern __shared__ __align__(16) char lds[];
@@ -503,7 +516,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void down_kernel(MoeParams p) {
   // this wave's run of (slot, unit of k)
   const uint32_t share = part * kWaves + wave, shares = p.parts * kWaves;
   const int first = jobs * share / shares, end = jobs * (share + 1) / shares;
-  constexpr int kH = STEPS * RQ * 1024, kWave = kH + kPieceLds<STEPS>;
+  constexpr int kH = kDownH<RQ, STEPS>, kWave = kH + kPieceLds<STEPS>;
   char *hl = lds + wave * kWave, *wl = hl + kH;
   // [wave][token][16]: this wave's sums
   f32x4* y = reinterpret_cast<f32x4*>(lds + kWaves * kWave) + wave * p.M * 4;
@@ -512,23 +525,24 @@ __global__ __launch_bounds__(64 * kWaves, 4) void down_kernel(MoeParams p) {
   if (first < end) {
     struct Unit {
       Piece<STEPS> w;
-      XRows<RQ> hi[STEPS], lo[STEPS];
+      XRows<RQ> h[3][STEPS];
     } buf[U];
     // what is loaded next
     const uint32_t row_bytes = p.I / 2, code_row = (lane >> 2) * row_bytes, scale_row = (lane >> 2) * nb;
     const int slot0 = first / units;
     int job = first, slot = slot0, unit = first - slot0 * units;
     const uint8_t *codes, *scales;
-    const uint16_t *hi, *lo;
+    const uint16_t* h;
+    const size_t plane = size_t(p.M) * (p.top + p.S) * p.I;
     uint32_t row[RQ];
     int n_load = 0, n_use = 0;  // of the slot that is loaded and of the one that is used
     const auto aim = [&]() {
       const SlotView s(p.slot + slot);
       n_load = s.n;
-      const size_t r = size_t(s.expert) * p.K + n0, at = size_t(s.begin) * p.I;
+      const size_t r = size_t(s.expert) * p.K + n0;
       codes = p.w_down + r * row_bytes;
       scales = p.s_down + r * nb;
-      hi = p.h_hi + at, lo = p.h_lo + at;
+      h = p.h + size_t(s.begin) * p.I;
 #pragma unroll
       for (int q = 0; q < RQ; ++q) row[q] = uint32_t(min(4 * q + g, s.n - 1)) * (p.I * 2);
     };
@@ -536,10 +550,10 @@ __global__ __launch_bounds__(64 * kWaves, 4) void down_kernel(MoeParams p) {
       if (job == end) return;
       load_piece<STEPS, TINY>(b.w, codes, code_row, scales, scale_row, nb, unit, lane & 3);
 #pragma unroll
-      for (int j = 0; j < STEPS; ++j) {
-        load_x<RQ>(b.hi[j], hi, row, (unit * STEPS + j) * 128, p.I, l16, n_load);
-        load_x<RQ>(b.lo[j], lo, row, (unit * STEPS + j) * 128, p.I, l16, n_load);
-      }
+      for (int j = 0; j < STEPS; ++j)
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          load_x<RQ>(b.h[i][j], h + i * plane, row, (unit * STEPS + j) * 128, p.I, l16, n_load);
       if (++job < end && ++unit == units) {
         unit = 0;
         ++slot;
@@ -549,32 +563,43 @@ __global__ __launch_bounds__(64 * kWaves, 4) void down_kernel(MoeParams p) {
     f32x4 acc = {};
     const auto use = [&](Unit& b, int unit) {
       stage_piece<STEPS, TINY>(wl, b.w, nb, unit, lane);
-#pragma unroll
-      for (int j = 0; j < STEPS; ++j)
-        stage_x<RQ>(hl + j * (RQ * 1024), b.hi[j], (unit * STEPS + j) * 128, p.I, l16, g, n_use);
-      wave_lds_fence();
-      bf16x8 w[STEPS][4];
-#pragma unroll
-      for (int j = 0; j < STEPS; ++j) {
+      const auto weights = [&](int j, bf16x8(&w)[4]) {
         const float sc = scale_of(scale_operand<STEPS>(wl, j, l16, g));
         const u32x4 c = codes_operand(wl, j, l16, g);
 #pragma unroll
-        for (int d = 0; d < 4; ++d) w[j][d] = dequant8(c[d], sc);
+        for (int d = 0; d < 4; ++d) w[d] = dequant8(c[d], sc);
+      };
+      if (RQ == 1) {
+        const int r = l16 < 12 ? l16 : l16 - 4;  // (the last four columns are not used)
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j) {
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            stage_x<RQ>(hl, b.h[i][j], (unit * STEPS + j) * 128, p.I, l16, g, n_use, 4 * i);
+          wave_lds_fence();
+          bf16x8 w[4];
+          weights(j, w);
+#pragma unroll
+          for (int d = 0; d < 4; ++d) acc = mfma32(w[d], x_operand_of(hl, r, d, g), acc);
+          wave_lds_fence();
+        }
+        return;
       }
-      const auto multiply = [&]() {
+      bf16x8 w[STEPS][4];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
 #pragma unroll
         for (int j = 0; j < STEPS; ++j)
+          stage_x<RQ>(hl + j * (RQ * 1024), b.h[i][j], (unit * STEPS + j) * 128, p.I, l16, g, n_use);
+        wave_lds_fence();
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j) {
+          if (i == 0) weights(j, w[j]);
 #pragma unroll
           for (int d = 0; d < 4; ++d) acc = mfma32(w[j][d], x_operand<RQ>(hl + j * (RQ * 1024), d, l16, g), acc);
-      };
-      multiply();
-      wave_lds_fence();
-#pragma unroll
-      for (int j = 0; j < STEPS; ++j)
-        stage_x<RQ>(hl + j * (RQ * 1024), b.lo[j], (unit * STEPS + j) * 128, p.I, l16, g, n_use);
-      wave_lds_fence();
-      multiply();
-      wave_lds_fence();
+        }
+        wave_lds_fence();
+      }
     };
     int at = first, at_slot = slot0, at_unit = unit;
     const auto step = [&](Unit& b) {
@@ -583,6 +608,10 @@ __global__ __launch_bounds__(64 * kWaves, 4) void down_kernel(MoeParams p) {
       ++at;
       if (++at_unit == units || at == end) {
         const SlotView s(p.slot + at_slot);
+        if (RQ == 1) {  // columns t, 4 + t and 8 + t
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i] += __shfl_xor(acc[i], 4) + __shfl_xor(acc[i], 8);
+        }
         if (l16 < s.n) y[s.token(l16) * 4 + g] += acc;
         wave_lds_fence();
         acc = f32x4{};
@@ -674,8 +703,7 @@ MoeLayout moe_layout(int M, int K, int I, int E, int S, int top) {
   l.logits = part(size_t(l.slices) * M * E * 8);
   l.slot = part(size_t(moe_slots(M, E, S, top, 4)) * sizeof(MoeSlot));
   l.pair_gate = part((pairs + 16) * 4);
-  l.h_hi = part(pairs * I * 2);
-  l.h_lo = part(pairs * I * 2);
+  l.h = part(pairs * I * 3 * 2);
   l.sums = part(most > 1 ? most * M * K * 4 : 0);
   l.total = at;
   return l;
@@ -713,12 +741,12 @@ hipError_t launch_moe(const MoeParams& params, int cus, hipStream_t st) {
     e = go(p.K < 128 ? &up_kernel<1, 2, 2, true> : &up_kernel<1, 2, 2, false>, up, 64 * kWaves, 0);
     if (e != hipSuccess) return e;
     return go(p.I < 128 ? &down_kernel<1, 2, 1, true> : &down_kernel<1, 2, 1, false>, down, 64 * kWaves,
-              sums + kWaves * (2048 + kPieceLds<2>));
+              sums + kWaves * (kDownH<1, 2> + kPieceLds<2>));
   }
   e = go(p.K < 128 ? &up_kernel<4, 1, 1, true> : &up_kernel<4, 1, 1, false>, up, 64 * kWaves, 0);
   if (e != hipSuccess) return e;
   return go(p.I < 128 ? &down_kernel<4, 1, 1, true> : &down_kernel<4, 1, 1, false>, down, 64 * kWaves,
-            sums + kWaves * (4096 + kPieceLds<1>));
+            sums + kWaves * (kDownH<4, 1> + kPieceLds<1>));
 }
 
 }  // namespace kda

@@ -160,8 +160,7 @@ kda_status_t kda_mx4_moe(const void* x, const void* router, const float* router_
   p.done = reinterpret_cast<int32_t*>(ws + lay.done);
   p.slot = reinterpret_cast<kda::MoeSlot*>(ws + lay.slot);
   p.pair_gate = reinterpret_cast<float*>(ws + lay.pair_gate);
-  p.h_hi = reinterpret_cast<uint16_t*>(ws + lay.h_hi);
-  p.h_lo = reinterpret_cast<uint16_t*>(ws + lay.h_lo);
+  p.h = reinterpret_cast<uint16_t*>(ws + lay.h);
   p.sums = reinterpret_cast<float*>(ws + lay.sums);
   int cus = 0;
   if (hipError_t e = kda::device_cus(&cus); e != hipSuccess) return failed(e, "device query");

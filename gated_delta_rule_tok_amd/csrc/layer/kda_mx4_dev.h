@@ -129,9 +129,10 @@ __device__ __forceinline__ void load_x(XRows<RQ>& x, const uint16_t* base, const
     if (RQ == 1 || 4 * q < n)
       x.v[q] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(at) + (row[q] + uint32_t(min(l16, rest)) * 16));
 }
-// Pieces behind the end of k (they repeat another) as zeros.
+// Pieces behind the end of k (they repeat another) as zeros.  row0: row of LDS of the first.
 template <int RQ>
-__device__ __forceinline__ void stage_x(char* lds, XRows<RQ>& x, int k0, int K, int l16, int g, int n = 4 * RQ) {
+__device__ __forceinline__ void stage_x(char* lds, XRows<RQ>& x, int k0, int K, int l16, int g, int n = 4 * RQ,
+                                        int row0 = 0) {
   if (k0 + 128 > K) {
     const bool in = k0 + 8 * l16 < K;
 #pragma unroll
@@ -140,15 +141,17 @@ __device__ __forceinline__ void stage_x(char* lds, XRows<RQ>& x, int k0, int K, 
   }
 #pragma unroll
   for (int q = 0; q < RQ; ++q) {
-    const int r = 4 * q + g;
+    const int r = row0 + 4 * q + g;
     if (RQ == 1 || 4 * q < n) *reinterpret_cast<u32x4*>(lds + r * 256 + ((l16 ^ r) << 4)) = x.v[q];
   }
+}
+__device__ __forceinline__ bf16x8 x_operand_of(const char* lds, int r, int d, int g) {
+  return *reinterpret_cast<const bf16x8*>(lds + r * 256 + (((4 * g + d) ^ r) << 4));
 }
 // (rows that are not staged repeat those that are: their columns are not used)
 template <int RQ>
 __device__ __forceinline__ bf16x8 x_operand(const char* lds, int d, int l16, int g) {
-  const int r = l16 & (4 * RQ - 1);
-  return *reinterpret_cast<const bf16x8*>(lds + r * 256 + (((4 * g + d) ^ r) << 4));
+  return x_operand_of(lds, l16 & (4 * RQ - 1), d, g);
 }
 // Orders the wave's own LDS accesses (they complete in order) for the compiler.
 __device__ __forceinline__ void wave_lds_fence() {

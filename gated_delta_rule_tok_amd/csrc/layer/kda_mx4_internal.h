@@ -60,12 +60,12 @@ struct MoeParams {
   int32_t* done;          // [K / 16]: parts of down's sums that are there
   MoeSlot* slot;
   float* pair_gate;       // [M (top + S) + 16]
-  uint16_t *h_hi, *h_lo;  // [M (top + S)][I]: silu(G x) * (U x) as two bf16 pieces
+  uint16_t* h;            // [3][M (top + S)][I]: gate * silu(G x) * (U x) as three bf16 pieces
   float* sums;            // [parts][M][K]
 };
 struct MoeLayout {
   int slices, slice_blocks;
-  size_t logits, head, done, slot, pair_gate, h_hi, h_lo, sums, total;
+  size_t logits, head, done, slot, pair_gate, h, sums, total;
 };
 // Slots that a call may have, at most.
 int moe_slots(int M, int E, int S, int top, int chunk);

@@ -120,9 +120,9 @@ typedef enum { KDA_ROUTE_SIGMOID = 0, KDA_ROUTE_SOFTMAX = 1 } kda_route_t;
  *
  * Numerics.  The router's products, sums and scores are fp64, so that the choice
  * is that of the formula for scores that differ by more than about 1e-15 of the
- * logits' terms.  G x and U x are fp32 sums of exact products; their product
- * enters W_down as two bf16 pieces (16 bits); sums over inter and over experts
- * are fp32, and out is rounded once.  An infinity or a NaN in x or in an expert's
+ * logits' terms.  G x and U x are fp32 sums of exact products; gate silu(G x) (U x)
+ * is an fp32 number that enters W_down with all of its bits (as three bf16 pieces);
+ * sums over inter and over experts are fp32, and out is rounded once.  An infinity or a NaN in x or in an expert's
  * weights leaves the choice well defined (a score of NaN is never taken before a
  * number) and makes the rows of out that read it NaN or infinite; other rows are
  * not affected.  Where the chosen scores add up to 0, renormalise gives NaN.
