@@ -145,7 +145,8 @@ constexpr int kMaxSlots = 64 * 32 + 16 * 16;
 // The experts that are hit, in order, with their tokens in order; shared experts
 // behind them.  One workgroup.
 struct RouteLds {
-  double key[kMaxExperts], score[kMaxExperts], red[kRouteThreads / 64], chosen[32];
+  double key[kMaxExperts], next[kMaxExperts];  // the order: of the sums, then of the logits
+  double score[kMaxExperts], red[kRouteThreads / 64], chosen[32];
   int chosen_id[32];
   int16_t best[kMaxExperts / 64 * 32];
 };
@@ -212,19 +213,33 @@ __device__ void list_slots(const MoeParams& p, ListLds& L) {
   for (int i = t; i < p.S * lives; i += kRouteThreads) p.pair_gate[lives * p.top + i] = 1.f;
 }
 
-// The top largest keys, of equal ones the first: each wave ranks 64 adjacent experts at a
-// time, then the best of those are ranked among each other.
+// Numbers in the order of v (logits and sums; finite ones are far from 1e300), a NaN behind
+// minus infinity.
+__device__ __forceinline__ double order_of(double v) {
+  return v != v ? -INFINITY : v == -INFINITY ? -1e300 : v;
+}
+// Of two experts whose sums are the same: whether f comes before e.
+__device__ __forceinline__ bool next_before(const RouteLds& L, int f, int e) {
+  const double a = L.next[f], b = L.next[e];
+  return a > b || (a == b && f < e);
+}
+// The top largest keys, of equal ones the largest next, of equal ones of these the first:
+// each wave ranks 64 adjacent experts at a time, then the best of those are ranked among
+// each other.
 __device__ __forceinline__ void choose(const MoeParams& p, RouteLds& L, int m) {
   const int t = threadIdx.x, lane = t & 63;
   for (int e0 = t & ~63; e0 < p.E; e0 += kRouteThreads) {
     const int e = e0 + lane, end = min(64, p.E - e0);
     const double v = L.key[min(e, p.E - 1)];
-    int rank = 0;
+    int rank = 0, same = 0;
 #pragma unroll 8
     for (int i = 0; i < end; ++i) {
       const double o = L.key[e0 + i];
-      rank += o > v || (o == v && i < lane) ? 1 : 0;
+      rank += o > v ? 1 : 0;
+      same += o == v ? 1 : 0;
     }
+    if (lane < end && same > 1)
+      for (int i = 0; i < end; ++i) rank += L.key[e0 + i] == v && next_before(L, e0 + i, e) ? 1 : 0;
     if (lane < end && rank < p.top) L.best[(e0 >> 6) * p.top + rank] = int16_t(e);
   }
   __syncthreads();
@@ -232,13 +247,15 @@ __device__ __forceinline__ void choose(const MoeParams& p, RouteLds& L, int m) {
   for (int i = t; i < n; i += kRouteThreads) {
     const int e = L.best[i];
     const double v = L.key[e];
-    int rank = 0;
+    int rank = 0, same = 0;
 #pragma unroll 4
     for (int j = 0; j < n; ++j) {
-      const int f = L.best[j];
-      const double o = L.key[f];
-      rank += o > v || (o == v && f < e) ? 1 : 0;
+      const double o = L.key[L.best[j]];
+      rank += o > v ? 1 : 0;
+      same += o == v ? 1 : 0;
     }
+    if (same > 1)
+      for (int j = 0; j < n; ++j) rank += L.key[L.best[j]] == v && next_before(L, L.best[j], e) ? 1 : 0;
     if (rank < p.top) {
       L.chosen[rank] = L.score[e];
       L.chosen_id[rank] = e;
@@ -252,7 +269,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeParams p) {
     RouteLds route;
     ListLds list;
   } L;
-  double *key = L.route.key, *score = L.route.score, *red = L.route.red, *chosen = L.route.chosen;
+  double *score = L.route.score, *red = L.route.red, *chosen = L.route.chosen;
+  double *key = L.route.key, *next = L.route.next;
   int* chosen_id = L.route.chosen_id;
   const int m = blockIdx.x, t = threadIdx.x;
   if (p.idx && p.idx[m] < 0) {
@@ -274,7 +292,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeParams p) {
       double sum = 0;
       for (int e = t; e < p.E; e += kRouteThreads) {
         const double l = score[e];
-        key[e] = l;
+        next[e] = order_of(l);
         score[e] = exp(l - most);
         sum += score[e];
       }
@@ -283,15 +301,17 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeParams p) {
     } else {
       for (int e = t; e < p.E; e += kRouteThreads) {
         const double l = score[e];
-        key[e] = l;
+        next[e] = order_of(l);
         score[e] = 1.0 / (1.0 + exp(-l));
       }
     }
-    // The order is that of the scores plus the bias; without one the logits have the
-    // same, also where scores have run into 0 or 1.  No NaN comes before a number.
+    // The order is that of the scores plus the bias.  Where 64 bits hold two sums as the
+    // same (scores that have run into 0 or 1, or a bias that is far larger) that of the
+    // logits, which is theirs for equal biases; sums that are infinite are the same indeed.
     for (int e = t; e < p.E; e += kRouteThreads) {
-      const double v = p.bias ? score[e] + double(p.bias[e]) : key[e];
-      key[e] = v == v ? v : -INFINITY;
+      const double v = score[e] + (p.bias ? double(p.bias[e]) : 0.0);
+      key[e] = order_of(v);
+      if (isinf(v)) next[e] = 0;
     }
     __syncthreads();
     choose(p, L.route, m);

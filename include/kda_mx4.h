@@ -88,7 +88,7 @@ typedef enum { KDA_ROUTE_SIGMOID = 0, KDA_ROUTE_SOFTMAX = 1 } kda_route_t;
  *     l_e   =  sum_k x[k] router[e, k]
  *     p_e   =  1 / (1 + exp(-l_e)), or exp(l_e) / sum_f exp(l_f)
  *     ids   =  the top_k experts with the largest p_e + router_bias[e], largest
- *              first, of equal ones the lowest index
+ *              first, of equal ones the lowest index (see below)
  *     gate_j = route_scale * p_(ids j) [ / sum_i p_(ids i) with renormalise ]
  *     f_e(x) =  W_down,e (silu(G_e x) * (U_e x)),  silu(a) = a / (1 + exp(-a))
  *     out   =  bf16( sum_j gate_j f_(ids j)(x) + sum_s f_(experts + s)(x) )
@@ -120,11 +120,13 @@ typedef enum { KDA_ROUTE_SIGMOID = 0, KDA_ROUTE_SOFTMAX = 1 } kda_route_t;
  *
  * Numerics.  The router's products, sums and scores are fp64, so that the choice
  * is that of the formula for scores that differ by more than about 1e-15 of the
- * logits' terms.  G x and U x are fp32 sums of exact products; gate silu(G x) (U x)
+ * logits' terms.  Where fp64 holds two finite sums p_e + router_bias[e] as the same,
+ * the larger logit comes first (scores of sigmoid that are 1 to the last bit, those
+ * beside a bias of 1e30), and of equal logits the lowest index; of infinite sums
+ * the lowest index.  A sum of NaN comes behind all others.  G x and U x are fp32 sums of exact products; gate silu(G x) (U x)
  * is an fp32 number that enters W_down with all of its bits (as three bf16 pieces);
  * sums over inter and over experts are fp32, and out is rounded once.  An infinity or a NaN in x or in an expert's
- * weights leaves the choice well defined (a score of NaN is never taken before a
- * number) and makes the rows of out that read it NaN or infinite; other rows are
+ * weights leaves the choice well defined and makes the rows of out that read it NaN or infinite; other rows are
  * not affected.  Where the chosen scores add up to 0, renormalise gives NaN.
  */
 size_t kda_mx4_moe_workspace_size(int32_t max_tokens, int32_t k, int32_t inter, int32_t experts,
