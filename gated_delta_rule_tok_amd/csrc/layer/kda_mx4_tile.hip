@@ -31,11 +31,14 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // 16 bytes per lane from base + soff + voff to LDS at lds + more + 16 * lane
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // (m0 is reserved: no variable is ever in it)
 __device__ __forceinline__ void load_lds(i32x4 base, uint32_t voff, uint32_t soff, uint32_t lds, uint32_t more) {
   asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :: "s"(lds), "v"(voff), "s"(base), "s"(soff), "i"(more)
-               : "memory", "scc");
+               : "memory", "scc", "m0");
 }
+#pragma clang diagnostic pop
 // bytes: behind them loads give zeros
 __device__ __forceinline__ i32x4 rsrc_of(const void* p, uint64_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(p);
