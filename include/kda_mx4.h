@@ -68,13 +68,16 @@ kda_status_t kda_mx4_dequant(const void* codes, const void* scales, void* out, v
  * 2^30 (for one row any); ceil(num_tokens / 256) * ceil(n / 256) < 2^23.  y must
  * not overlap x or w.
  *
- * Every product is exact (with bf16 x of weights below 2^128, which bf16 holds),
- * sums are fp32 (up to 128 products at a time in one instruction, whose own sum
- * is off by less than 2^-24 of the products' magnitudes).  A value of x that is not
- * finite, or a scale of NaN, makes its token's row of y, or its weight row's column,
- * NaN or infinite; others are not affected.  The order of a sum may depend on
- * num_tokens, and on nothing else of the other tokens.  No workspace.  x and y may be
- * NULL when num_tokens is 0.
+ * Products and sums are fp32: every product between 2^-126 and 2^128 in magnitude is
+ * exact, what is smaller may count as 0, and what is larger is infinite, as are, with
+ * bf16 x, weights of 2^128 and more (s = 253 and 254).  Up to 128 products at a time
+ * are added in one instruction, whose own sum is off by less than 2^-24 of their
+ * magnitudes.  A value of x that is not finite, or a scale of NaN, makes its token's
+ * row of y, or its weight row's column, NaN or infinite; others are not affected.
+ * The order of a sum may depend on num_tokens, and on nothing else of the other
+ * tokens.  Of the scales the whole aligned 4-byte words may be read in which those of
+ * an operand begin and end; what else is in them has no effect.  No workspace.  x and
+ * y may be NULL when num_tokens is 0.
  */
 kda_status_t kda_mx4_proj(const void* x, const void* x_scales, const void* w, const void* w_scales,
                           void* y, void* stream, int64_t num_tokens, int32_t k, int32_t n,
@@ -118,16 +121,21 @@ typedef enum { KDA_ROUTE_SIGMOID = 0, KDA_ROUTE_SOFTMAX = 1 } kda_route_t;
  * router, w_up, w_down and out 16-byte aligned, x_row and out_row multiples of 8
  * between k and 2^24 (for one row any).
  *
- * Numerics.  The router's products, sums and scores are fp64, so that the choice
- * is that of the formula for scores that differ by more than about 1e-15 of the
- * logits' terms.  Where fp64 holds two finite sums p_e + router_bias[e] as the same,
- * the larger logit comes first (scores of sigmoid that are 1 to the last bit, those
- * beside a bias of 1e30), and of equal logits the lowest index; of infinite sums
- * the lowest index.  A sum of NaN comes behind all others.  G x and U x are fp32 sums of exact products; gate silu(G x) (U x)
- * is an fp32 number that enters W_down with all of its bits (as three bf16 pieces);
- * sums over inter and over experts are fp32, and out is rounded once.  An infinity or a NaN in x or in an expert's
- * weights leaves the choice well defined and makes the rows of out that read it NaN or infinite; other rows are
- * not affected.  Where the chosen scores add up to 0, renormalise gives NaN.
+ * Numerics.  The router's products, sums and scores are fp64, so that the choice is
+ * that of the formula for scores that differ by more than about 1e-15 of the
+ * logits' terms, and a token's ids and gates do not depend on the other tokens.
+ * Where fp64 holds two finite sums p_e + router_bias[e] as the same (scores of
+ * sigmoid that are 1 to the last bit, those beside a bias of 1e30), the larger
+ * logit comes first, and of equal logits the lowest index; of infinite sums the
+ * lowest index.  A sum of NaN comes behind all others.  G x and U x are fp32 sums,
+ * with the range of kda_mx4_proj for bf16 x; gate silu(G x) (U x) is an fp32 number
+ * that enters W_down with all of its bits (as three bf16 pieces; what of it is
+ * below 2^-133 is lost); sums over inter and over experts are fp32, in an order
+ * that depends on which experts the other tokens take (the last bits of out do,
+ * too), and out is rounded once.  An infinity or a NaN in x or in an expert's
+ * weights leaves the choice well defined and makes the rows of out that read it NaN
+ * or infinite; it does not enter other rows.  Where the chosen scores add up to 0,
+ * renormalise gives NaN.
  */
 size_t kda_mx4_moe_workspace_size(int32_t max_tokens, int32_t k, int32_t inter, int32_t experts,
                                   int32_t shared, int32_t top_k);
