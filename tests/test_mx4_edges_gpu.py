@@ -1,12 +1,14 @@
-"""The experts' layer (include/kda_mx4.h) where it can go wrong without any result
-looking odd: inputs whose exact answer is a small whole number or an order."""
+"""The operators of include/kda_mx4.h where they can go wrong without any result looking
+odd: the experts' layer on inputs whose exact answer is a small whole number or an
+order and on weights beyond 4 GiB; tiles with rows of y in whole pieces that n does not
+fill, and with scales and k that are read as they lie."""
 from __future__ import annotations
 
 import math
 
 import pytest
 
-from test_mx4_gpu import Moe
+from test_mx4_gpu import Moe, _check_product, _kda, _values, _weights
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +125,54 @@ def test_infinite_biases():
     assert torch.equal(p.ids[:, :2].cpu(), torch.tensor([1, 3], dtype=torch.int32).expand(4, -1))
     assert torch.equal(p.ids[:, 5:].cpu(), torch.tensor([5, 6, 7], dtype=torch.int32).expand(4, -1))
     p.check("infinite biases")
+
+
+def test_experts_beyond_4_gib():
+    """Rows of W_up and W_down whose offsets pass 32 bits: the experts behind them, and some in
+    front."""
+    import torch
+    p = Moe(5, 4096, 4096, 620, 4, 2, True, seed=97)
+    assert p.w_down.numel() > 1 << 32 and p.w_up.numel() > 1 << 33 and p.s_up.numel() > 1 << 29
+    p.bias[:] = -1
+    p.bias[[0, 250, 300, 515, 619]] = torch.tensor([1.0, 1.1, 1.2, 1.3, 1.4], device="cuda")
+    p.run().check("large experts")
+    assert (p.ids >= 512).any() and (p.ids < 512).any()
+    q = Moe(40, 4096, 4096, 620, 4, 2, True, seed=97)
+    q.bias[:] = -1
+    q.bias[610:] = 0
+    q.run().check("large experts, many tokens")
+    assert (q.ids >= 610).all()
+
+
+# (64 x 64, 128 x 128 and 256 x 256 tiles on 256 compute units, the scales as they lie and turned)
+@pytest.mark.parametrize("m,k,n", [(300, 512, 2051), (300, 544, 2053), (300, 1024, 8195), (300, 1056, 8198),
+                                   (1100, 256, 8197), (1100, 288, 8201), (70, 128, 16007)])
+def test_rows_of_y_in_whole_pieces(m, k, n):
+    """y_row a multiple of 8 and n none: 16-byte stores and single ones in a row; what is behind
+    n, and behind the last row, stays."""
+    import torch
+    x, xs = _weights((m,), k, m + k, spread=3)
+    w, ws = _weights((n,), k, n)
+    row = (n + 15) // 8 * 8
+    y = torch.full((m + 2, row), 3.0, dtype=torch.bfloat16, device="cuda")
+    _kda().kda_mx4_proj(x, xs, w, ws, y[:m, :n])
+    _check_product(_values(x, xs), w, ws, y[:m, :n], f"pieces {m}x{k}x{n}")
+    assert (y[m:] == 3).all() and (y[:, n:] == 3).all()
+
+
+@pytest.mark.parametrize("m,k,n", [(300, 512, 2100), (300, 1024, 8200), (1100, 512, 8200), (70, 128, 16000)])
+def test_rows_of_whole_stages_do_not_mix(m, k, n):
+    """A NaN scale of a token and of a weight row stay in their row and column where k is whole
+    stages and scales lie at whole words: first, last and middle blocks."""
+    import torch
+    x, xs = _weights((m,), k, 60)
+    w, ws = _weights((n,), k, 61)
+    y, z = (torch.empty(m, n, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    _kda().kda_mx4_proj(x, xs, w, ws, y)
+    for tokens, rows, block in ([0, m - 1], [5, n - 1], 0), ([63, 64], [64, n - 2], k // 32 - 1), ([17], [n // 2], k // 64):
+        xn, wn = xs.clone(), ws.clone()
+        xn[tokens, block] = wn[rows, block] = 255
+        _kda().kda_mx4_proj(x, xn, w, wn, z)
+        hit = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+        hit[tokens] = hit[:, rows] = True
+        assert z[hit].isnan().all() and torch.equal(z[~hit], y[~hit])
