@@ -735,12 +735,14 @@ MoeLayout moe_layout(int M, int K, int I, int E, int S, int top) {
 
 hipError_t launch_moe(const MoeParams& params, int cus, hipStream_t st) {
   MoeParams p = params;
-  // Tokens per slot: 4 where an expert that is hit has about two at most.  us with 4 / 16,
-  // all experts as likely: 7168 x 512, 8 + 1 of 256 experts, 16 tokens 155 / 200, 64 tokens
-  // 341 / 406; 2048 x 1024, 8 of 128, 32 tokens 104 / 114, 64 tokens 149 / 135; 2080 x 1056,
-  // 4 of 40, 32 tokens 75 / 70.  What has more tokens than a slot is read once for each
-  // slot, from the L2 mostly: by workgroups that run at the same time.
-  p.chunk = p.M <= 4 || p.M * p.top <= 2 * p.E ? 4 : 16;
+  // Tokens per slot: 4 where an expert has about three at most (of all rows, padding among
+  // them: the host knows no better).  us with 4 / 16, all experts as likely: 7168 x 512,
+  // 8 + 1 of 256 experts, 16 tokens 160 / 224, 64 tokens 361 / 453; 4096 x 1024, 4 + 1 of
+  // 64, 40 tokens 134 / 151; 2048 x 1024, 8 of 128, 32 tokens 110 / 128, 64 tokens 149 /
+  // 149; 2080 x 1056, 4 of 40, 21 tokens 67 / 70, 32 tokens 75 / 75, 64 tokens 107 / 91.
+  // What has more tokens than a slot is read once for each slot, from the L2 mostly: by
+  // workgroups that run at the same time.
+  p.chunk = p.M <= 4 || p.M * p.top <= 3 * p.E ? 4 : 16;
   p.parts = moe_parts(p.M, p.K, p.I, p.E, p.S, p.top, p.chunk);
   void* args[] = {&p};
   const auto go = [&](auto* f, dim3 grid, int threads, size_t lds) {
