@@ -14,12 +14,12 @@
 // sum, and with a whole-number result there is no rounding to hide behind.  It
 // costs 0.75 us of the fp64 matrix pipe per 16 tokens at 256 x 7168.
 //
-// 7168 x 512, 8 + 1 of 256 experts: one token 31 us (logits 5, route 6.5, up 13.5, down 8:
-// each a launch and a chain of round trips, 50 MB in all), 64 tokens 315 to 345 us by how
-// many experts they hit (up 194 to 209, 4.2 TB/s; down 111 to 120, 3.7 TB/s; a copy
-// reaches 5.0).  What it took: whole lines through LDS instead of operands as they are
+// 7168 x 512, 8 + 1 of 256 experts: one token 30 us (logits 5.5, route 5.7, up 13.5, down
+// 8: each a launch and a chain of round trips, 50 MB in all), 64 tokens 335 to 361 us by
+// how many experts they hit (up 194, 4.2 TB/s; down 128, 3.2 TB/s: its third piece of h
+// costs 11 us; a copy reaches 5.0).  What it took: whole lines through LDS instead of operands as they are
 // wanted (404 to 286 us on tokens that hit half the experts: the address unit was the
-// bound), units of 256 of k in down (139 to 111: instructions were), short code, since
+// bound), units of 256 of k in down (139 to 111 then: instructions were), short code, since
 // single-token launches run each line of it once.
 #include "kda_mx4_dev.h"
 #include "kda_mx4_internal.h"

@@ -1,7 +1,7 @@
 // kda_mx4_tile.hip -- products of many rows x with weights, both in microscaled
 // 4-bit numbers:  y[m, n] = sum_k x[m, k] w[n, k].
 //
-// Bound by the scaled 4-bit MFMA (32x32x64: 32 cycles) where there are many rows.  A
+// The floor for many rows is the scaled 4-bit MFMA (32x32x64: 32 cycles).  A
 // workgroup makes BM x BN outputs from operands in LDS: stages of 128 of k that loads
 // fill directly, three or seven ahead of the one in use, and the scales of 512 of k at a
 // time.  A wave has the operands of its next half stage on the way while it issues the
@@ -11,8 +11,9 @@
 // load into LDS before each read of it, which leaves one stage in flight.  Their
 // count in flight is waited on by hand.
 //
-// 8192 x 7168 x 7168: 223 to 245 us by the card's clock (1.9 GHz under this load), 3.4 to
-// 3.8 PFLOP/s; the MFMAs are busy 46% of the time.  896 tiles on 256 units are four rounds
+// 8192 x 7168 x 7168: 226 us where the same call is repeated, 244 to 274 between other
+// kernels, 3.1 to 3.7 PFLOP/s; the MFMAs are busy 42 to 47% of the cycles, at 1.9 GHz (84
+// us would do at 2.4 GHz).  896 tiles on 256 units are four rounds
 // where 3.5 would do, a round's stores (6 us) overlap nothing, and a stage of 1024 MFMA
 // cycles takes about 1600 with a workgroup alone.  Steps: operands read where they are
 // used 271 us; read ahead of 16 MFMAs, but with a branch behind them, over which the
