@@ -17,10 +17,10 @@
 // 7168 x 512, 8 + 1 of 256 experts: one token 30 us (logits 5.5, route 5.7, up 13.5, down
 // 8: each a launch and a chain of round trips, 50 MB in all), 64 tokens 335 to 361 us by
 // how many experts they hit (up 194, 4.2 TB/s; down 128, 3.2 TB/s: its third piece of h
-// costs 11 us; a copy reaches 5.0).  What it took: whole lines through LDS instead of operands as they are
-// wanted (404 to 286 us on tokens that hit half the experts: the address unit was the
-// bound), units of 256 of k in down (139 to 111 then: instructions were), short code, since
-// single-token launches run each line of it once.
+// costs 11 us; a copy reaches 5.0).  What it took, each as measured then: whole lines
+// through LDS instead of operands as they are wanted (404 to 286 us on tokens that hit half
+// the experts: the address unit was the bound), units of 256 of k in down (139 to 111:
+// instructions were), short code, since single-token launches run each line of it once.
 #include "kda_mx4_dev.h"
 #include "kda_mx4_internal.h"
 
@@ -759,10 +759,11 @@ hipError_t launch_moe(const MoeParams& params, int cus, hipStream_t st) {
   const dim3 up(1u << p.up_log2), down(p.K / 16, p.parts);
   const size_t sums = size_t(kWaves) * p.M * 64;
   // Units of 256 of k with 4 tokens a slot: a unit costs about 100 instructions whatever
-  // its size, and down of 64 tokens, 7168 x 512, 256 experts, took 139 us with 128.  One in
-  // flight, but two in up, whose items are shorter: registers for other waves fill the time
-  // as well as loads ahead do (16 tokens a slot, 64 x 2080 x 1056, 40 experts 79 us against
-  // 85 with two).
+  // its size, and down of 64 tokens, 7168 x 512, 256 experts, took 139 us with 128 and 111
+  // with 256, both with two pieces of h.  One in flight, but two in up, whose items are
+  // shorter: registers for other waves fill the time as well as loads ahead do (16 tokens a
+  // slot, 64 x 2080 x 1056, 40 experts, two pieces of h: 79 us against 85 with two units;
+  // with three pieces two units do not fit in 128 registers).
   if (p.chunk == 4) {
     e = go(p.K < 128 ? &up_kernel<1, 2, 2, true> : &up_kernel<1, 2, 2, false>, up, 64 * kWaves, 0);
     if (e != hipSuccess) return e;
